@@ -29,11 +29,13 @@ EXPORTED = ["qsa_default_params", "qsa_status_string", "qsa_last_error", "qsa_in
             "qsa_decode_noalloc", "qsa_prefill_cached", "qsa_prefill_cached_workspace_size",
             "qsa_index_workspace_size", "qsa_decode_mean_pool", "qsa_mean_pool_keys",
             "qsa_decode_reuse", "qsa_verify", "qsa_verify_workspace_size", "qsa_set_decode_splits",
-            "qsa_decode_noalloc_check_error"]
+            "qsa_decode_noalloc_check_error", "qsa_default_layer_params", "qsa_norm_rope", "qsa_paged_append",
+            "qsa_paged_decode", "qsa_paged_prefill", "qsa_paged_workspace_size"]
 
 KERNEL_NAMES = {1: "rope_table", 2: "rope_k", 3: "indexer", 4: "select", 5: "attention", 6: "decode_append",
                 7: "decode_indexer", 8: "decode_attention", 9: "decode_combine",
-                10: "mean_pool_keys", 11: "verify_expand", 12: "idx_rope"}
+                10: "mean_pool_keys", 11: "verify_expand", 12: "idx_rope", 13: "norm_rope", 14: "paged_append",
+                15: "paged_decode", 16: "paged_decode_join", 17: "paged_prefill", 18: "paged_prefill_join"}
 
 
 class QSAError(RuntimeError):
@@ -51,6 +53,28 @@ class qsa_params(ctypes.Structure):
                 ("yarn_beta_fast", ctypes.c_double), ("yarn_beta_slow", ctypes.c_double),
                 ("idx_rope", ctypes.c_int32)]
 
+
+class qsa_layer_params(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("rope_axes", ctypes.c_int32),
+                ("rope_section", ctypes.c_int32 * 3), ("rope_interleaved", ctypes.c_int32),
+                ("rope_theta", ctypes.c_double), ("yarn_factor", ctypes.c_double),
+                ("yarn_original_max", ctypes.c_double), ("yarn_beta_fast", ctypes.c_double),
+                ("yarn_beta_slow", ctypes.c_double), ("norm_eps", ctypes.c_float),
+                ("norm_zero_centred", ctypes.c_int32), ("softmax_scale", ctypes.c_float), ("window", ctypes.c_int32),
+                ("n_sinks", ctypes.c_int32)]
+
+
+class qsa_paged_kv(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("table_ld", ctypes.c_int64)]
+
+
+# element types of the paged-cache calls (qsa_layer_params.dtype)
+DTYPE_BF16 = 0
+DTYPE_FP16 = 1
 
 # block-score aggregation (qsa_params.aggregation)
 AGG_TOKEN_MAX = 0
@@ -121,10 +145,18 @@ def _open(path: str):
     L.qsa_check_device_error.argtypes = [vp, vp]
     L.qsa_decode_noalloc_check_error.argtypes = [vp]
     L.qsa_set_decode_splits.argtypes = [i32]
+    LP, KV = ctypes.POINTER(qsa_layer_params), ctypes.POINTER(qsa_paged_kv)
+    L.qsa_default_layer_params.argtypes = [LP]
+    L.qsa_default_layer_params.restype = None
+    L.qsa_norm_rope.argtypes = [LP, i64, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp]
+    L.qsa_paged_append.argtypes = [LP, KV, i32, i64, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp]
+    L.qsa_paged_decode.argtypes = [LP, KV, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.qsa_paged_prefill.argtypes = [LP, KV, i32, i64, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.qsa_paged_workspace_size.argtypes = [LP, i32, i64, psz]
     L.qsa_trace_begin.argtypes = [i32]
     L.qsa_trace_end.argtypes = [vp, vp, i32, ctypes.POINTER(ctypes.c_int32)]
     for f in EXPORTED:
-        if f not in ("qsa_default_params", "qsa_status_string", "qsa_last_error"):
+        if f not in ("qsa_default_params", "qsa_default_layer_params", "qsa_status_string", "qsa_last_error"):
             getattr(L, f).restype = ctypes.c_int
     if hasattr(L, "qsa_debug_inject"):        # the debug build only
         L.qsa_debug_inject.argtypes = [i32]
@@ -293,6 +325,199 @@ def qsa_decode_noalloc(p: qsa_params, B: int, max_len: int, cache_len, k_cache, 
                                      _ptr(kidx_cache), _ptr(qidx_ring), _ptr(w_ring), _ptr(q_new), _ptr(k_new),
                                      _ptr(v_new), _ptr(q_idx_new), _ptr(k_idx_new), _ptr(w_new), _ptr(out),
                                      _ptr(sel_out), _ptr(lse_out), _stream(stream)), "qsa_decode_noalloc")
+
+
+# ------------------------------------------------- layers over a paged cache
+_TORCH_DTYPE = {DTYPE_BF16: (torch.bfloat16, torch.uint16), DTYPE_FP16: (torch.float16, torch.uint16)}
+
+
+def layer_params(n_q_heads: int = 24, n_kv_heads: int = 2, head_dim: int = 256, dtype=torch.bfloat16,
+                 rope_section=None, **kw) -> qsa_layer_params:
+    """qsa_layer_params with its defaults; ``dtype``: torch.bfloat16 or
+    torch.float16, ``rope_section``: rotary pairs of time, height, width."""
+    p = qsa_layer_params()
+    load().qsa_default_layer_params(ctypes.byref(p))
+    p.n_q_heads, p.n_kv_heads, p.head_dim = n_q_heads, n_kv_heads, head_dim
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("dtype must be torch.bfloat16 or torch.float16")
+    p.dtype = DTYPE_FP16 if dtype == torch.float16 else DTYPE_BF16
+    if rope_section is not None:
+        p.rope_section[:] = [int(x) for x in rope_section]
+    for k, v in kw.items():
+        if k not in _LAYER_FIELDS:
+            raise TypeError(f"qsa_layer_params has no field {k}")
+        setattr(p, k, v)
+    return p
+
+
+_LAYER_FIELDS = {n for n, _ in qsa_layer_params._fields_}
+
+
+class PagedKV:
+    """A paged cache of the paged calls: ``k_pages`` and ``v_pages``
+    [n_pages][page_size][n_kv_heads][head_dim] (any strides of whole 16-byte
+    units, alike for both; head-major pools pass ``pool.transpose(1, 2)``) and
+    ``page_table`` [B][max_pages] int32, all on one device.  Holds references to
+    the three tensors; ``c`` is the C struct."""
+
+    def __init__(self, k_pages, v_pages, page_table):
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
+            raise ValueError("k_pages and v_pages must be alike, [n_pages][page_size][n_kv_heads][head_dim]")
+        if k_pages.dtype != v_pages.dtype or k_pages.element_size() != 2:
+            raise ValueError("k_pages and v_pages must have one 16-bit dtype")
+        if k_pages.shape[3] > 1 and k_pages.stride(3) != 1:
+            raise ValueError("a page row's elements must be contiguous")
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or \
+                (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError("page_table must be int32 [B][max_pages] with contiguous rows")
+        if not (k_pages.device == v_pages.device == page_table.device):
+            raise ValueError("k_pages, v_pages and page_table must be on one device")
+        if 0 in k_pages.shape or page_table.shape[1] == 0:
+            raise ValueError("k_pages and page_table must not be empty")
+        self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
+        # the stride of a dimension of one entry is never used
+        d = k_pages.shape[3]
+        st = [s if n > 1 else max(d, s) // 8 * 8 for n, s in zip(k_pages.shape, k_pages.stride())]
+        ld = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+        self.c = qsa_paged_kv(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[0], k_pages.shape[1],
+                              page_table.shape[1], st[0], st[1], st[2], page_table.data_ptr(), ld)
+
+
+def _rows(t, what: str, p: qsa_layer_params, T: int, H: int, like):
+    """(pointer, row stride) of a [T][H][head_dim] tensor whose rows are contiguous inside."""
+    if t is None:
+        return None, 0
+    D = p.head_dim
+    if t.dim() != 3 or t.shape[0] < T or t.shape[1] != H or t.shape[2] != D:
+        raise ValueError(f"{what} must be [{T}][{H}][{D}], not {list(t.shape)}")
+    if t.dtype not in _TORCH_DTYPE[p.dtype]:
+        raise ValueError(f"{what} has dtype {t.dtype}, the layer {_TORCH_DTYPE[p.dtype][0]}")
+    if t.device != like:
+        raise ValueError(f"{what} is on {t.device}, not on {like}")
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"the heads of a row of {what} must be contiguous")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else H * D)
+
+
+def _flat(t, what: str, shape, dtypes, like):
+    """Pointer of a contiguous tensor of the given shape (rows may be more)."""
+    if t is None:
+        return None
+    if t.dim() != len(shape) or t.shape[0] < shape[0] or tuple(t.shape[1:]) != tuple(shape[1:]):
+        raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} has dtype {t.dtype}, not {dtypes[0]}")
+    if t.device != like:
+        raise ValueError(f"{what} is on {t.device}, not on {like}")
+    if not t.is_contiguous():
+        raise ValueError("QSA tensors must be contiguous")
+    return t.data_ptr()
+
+
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+
+
+def _positions(positions, p, T, like):
+    if positions is None:
+        return None
+    if p.rope_axes == 1 and positions.dim() == 1:
+        positions = positions[None]
+    if tuple(positions.shape) != (p.rope_axes, T):
+        raise ValueError(f"positions must be [{p.rope_axes}][{T}], not {list(positions.shape)}")
+    return _flat(positions, "positions", (p.rope_axes, T), _I32, like)
+
+
+def _paged(p, kv: PagedKV, B: int, ws):
+    """Checks of the cache against the layer; the cache's device."""
+    if kv.k_pages.shape[2] != p.n_kv_heads or kv.k_pages.shape[3] != p.head_dim:
+        raise ValueError(f"the pages hold {list(kv.k_pages.shape[2:])}, the layer [{p.n_kv_heads}, {p.head_dim}]")
+    if kv.k_pages.dtype not in _TORCH_DTYPE[p.dtype]:
+        raise ValueError(f"the pages have dtype {kv.k_pages.dtype}, the layer {_TORCH_DTYPE[p.dtype][0]}")
+    if kv.page_table.shape[0] < B:
+        raise ValueError(f"page_table has {kv.page_table.shape[0]} rows for {B} sequences")
+    dev = kv.k_pages.device
+    if ws is None or ws.device != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous workspace on the cache's device (paged_workspace)")
+    return dev
+
+
+def _on(dev, stream, call, where: str):
+    """``call(stream pointer)`` with ``dev`` current, on ``stream`` or on that device's current stream."""
+    if dev.type != "cuda":
+        raise ValueError(f"{where}: tensors are on {dev}, not on a CUDA device")
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return _check(call(_stream(stream)), where)
+    with torch.cuda.device(dev):
+        return _check(call(_stream(stream)), where)
+
+
+def qsa_norm_rope(p: qsa_layer_params, T: int, pos0: int, q, k, q_weight, k_weight, q_out, k_out, positions=None,
+                  stream=None):
+    """``q`` [T][n_q_heads][head_dim], ``k`` [T][n_kv_heads][head_dim] (row
+    strides free); ``q`` with ``q_out``, or ``k`` with ``k_out``, and each weight
+    may be None; ``positions`` int32 [rope_axes][T]."""
+    like = (q if q is not None else k).device
+    w = _TORCH_DTYPE[p.dtype]
+    (qp, ql), (kp, kl) = _rows(q, "q", p, T, p.n_q_heads, like), _rows(k, "k", p, T, p.n_kv_heads, like)
+    args = (_positions(positions, p, T, like), qp, ql, kp, kl, _flat(q_weight, "q_weight", (p.head_dim,), w, like),
+            _flat(k_weight, "k_weight", (p.head_dim,), w, like),
+            _flat(q_out, "q_out", (T, p.n_q_heads, p.head_dim), w, like),
+            _flat(k_out, "k_out", (T, p.n_kv_heads, p.head_dim), w, like))
+    _on(like, stream, lambda s: load().qsa_norm_rope(ctypes.byref(p), T, pos0, *args, s), "qsa_norm_rope")
+
+
+def qsa_paged_append(p: qsa_layer_params, kv: PagedKV, B: int, T: int, cu_new, cache_len, k, v, ws, q=None, q_out=None,
+                     q_weight=None, k_weight=None, positions=None, stream=None):
+    """``cu_new`` int32 [B + 1] or None (one token per sequence), ``cache_len``
+    int32 [B], both on the device."""
+    dev = _paged(p, kv, B, ws)
+    w = _TORCH_DTYPE[p.dtype]
+    (qp, ql), (kp, kl) = _rows(q, "q", p, T, p.n_q_heads, dev), _rows(k, "k", p, T, p.n_kv_heads, dev)
+    vp, vl = _rows(v, "v", p, T, p.n_kv_heads, dev)
+    args = (_flat(cu_new, "cu_new", (B + 1,), _I32, dev), _flat(cache_len, "cache_len", (B,), _I32, dev),
+            _positions(positions, p, T, dev), qp, ql, kp, kl, vp, vl,
+            _flat(q_weight, "q_weight", (p.head_dim,), w, dev), _flat(k_weight, "k_weight", (p.head_dim,), w, dev),
+            _flat(q_out, "q_out", (T, p.n_q_heads, p.head_dim), w, dev), ws.data_ptr(),
+            ws.numel() * ws.element_size())
+    _on(dev, stream, lambda s: load().qsa_paged_append(ctypes.byref(p), ctypes.byref(kv.c), B, T, *args, s),
+        "qsa_paged_append")
+
+
+def qsa_paged_decode(p: qsa_layer_params, kv: PagedKV, B: int, cache_len, q, out, ws, lse=None, stream=None):
+    """One new token per sequence (``q``, ``out`` [B][n_q_heads][head_dim])."""
+    dev = _paged(p, kv, B, ws)
+    w, shape = _TORCH_DTYPE[p.dtype], (B, p.n_q_heads, p.head_dim)
+    args = (_flat(cache_len, "cache_len", (B,), _I32, dev), _flat(q, "q", shape, w, dev),
+            _flat(out, "out", shape, w, dev), _flat(lse, "lse", shape[:2], _F32, dev), ws.data_ptr(),
+            ws.numel() * ws.element_size())
+    _on(dev, stream, lambda s: load().qsa_paged_decode(ctypes.byref(p), ctypes.byref(kv.c), B, *args, s),
+        "qsa_paged_decode")
+
+
+def qsa_paged_prefill(p: qsa_layer_params, kv: PagedKV, B: int, T: int, cu_new, cache_len, q, out, ws, lse=None,
+                      stream=None):
+    """T new tokens of B sequences (``q``, ``out`` [T][n_q_heads][head_dim])."""
+    dev = _paged(p, kv, B, ws)
+    w, shape = _TORCH_DTYPE[p.dtype], (T, p.n_q_heads, p.head_dim)
+    args = (_flat(cu_new, "cu_new", (B + 1,), _I32, dev), _flat(cache_len, "cache_len", (B,), _I32, dev),
+            _flat(q, "q", shape, w, dev), _flat(out, "out", shape, w, dev), _flat(lse, "lse", shape[:2], _F32, dev),
+            ws.data_ptr(), ws.numel() * ws.element_size())
+    _on(dev, stream, lambda s: load().qsa_paged_prefill(ctypes.byref(p), ctypes.byref(kv.c), B, T, *args, s),
+        "qsa_paged_prefill")
+
+
+def qsa_paged_workspace_size(p: qsa_layer_params, B: int, T: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().qsa_paged_workspace_size(ctypes.byref(p), B, T, ctypes.byref(n)), "qsa_paged_workspace_size")
+    return n.value
+
+
+def paged_workspace(p: qsa_layer_params, B: int, T: int, device="cuda") -> torch.Tensor:
+    """A workspace of the paged calls with its error word cleared."""
+    ws = torch.empty(qsa_paged_workspace_size(p, B, T), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
 
 
 def qsa_check_device_error(ws, stream=None) -> int:

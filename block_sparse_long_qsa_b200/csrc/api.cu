@@ -34,6 +34,14 @@ int64_t round4(int64_t x) { return (x + 3) / 4 * 4; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+template <class P>
+bool yarn_ok(const P* p) {
+  if (!std::isfinite(p->yarn_factor) || p->yarn_factor < 0.0) return false;
+  return !(p->yarn_factor > 1.0) || (p->yarn_original_max >= 1.0 && std::isfinite(p->yarn_original_max) &&
+                                     p->yarn_beta_slow > 0.0 && p->yarn_beta_fast > p->yarn_beta_slow &&
+                                     std::isfinite(p->yarn_beta_fast));
+}
+
 qsa_status check_params(const qsa_params* p) {
   if (!p) return QSA_ERR_INVALID_ARG;
   if (p->n_q_heads != 24 || p->n_kv_heads != 2 || p->head_dim != 256 || p->rope_dim != 64 || p->idx_heads != 4 ||
@@ -43,11 +51,7 @@ qsa_status check_params(const qsa_params* p) {
   if (p->budget_blocks < 2 || p->budget_blocks > 4096) return QSA_ERR_UNSUPPORTED;
   if (!(p->softmax_scale >= 0.f) || !std::isfinite(p->softmax_scale)) return QSA_ERR_INVALID_ARG;
   if (p->aggregation != QSA_AGG_TOKEN_MAX && p->aggregation != QSA_AGG_MEAN_POOL) return QSA_ERR_INVALID_ARG;
-  if (!std::isfinite(p->yarn_factor) || p->yarn_factor < 0.0) return QSA_ERR_INVALID_ARG;
-  if (p->yarn_factor > 1.0 && !(p->yarn_original_max >= 1.0 && std::isfinite(p->yarn_original_max) &&
-                                p->yarn_beta_slow > 0.0 && p->yarn_beta_fast > p->yarn_beta_slow &&
-                                std::isfinite(p->yarn_beta_fast)))
-    return QSA_ERR_INVALID_ARG;
+  if (!yarn_ok(p)) return QSA_ERR_INVALID_ARG;
   if (p->idx_rope != 0 && p->idx_rope != 1) return QSA_ERR_INVALID_ARG;
   if (p->idx_rope && p->aggregation != QSA_AGG_MEAN_POOL) return QSA_ERR_INVALID_ARG;
   return QSA_OK;
@@ -63,12 +67,14 @@ float softmax_scale(const qsa_params* p) {
   return p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)p->head_dim);
 }
 
-// Rotary frequencies of the 32 pairs, with static YaRN when yarn_factor > 1:
-// the pair index where the number of rotations over the original context,
-// L f_i / (2 pi), equals n is d ln(L / (2 pi n)) / (2 ln theta); pairs before
-// the beta_fast index (rounded down) keep f_i, pairs after the beta_slow index
-// (rounded up) take f_i / s, linear in the index in between.
-void inv_freq(const qsa_params* p, double* f) {
+// Rotary frequencies of the rope_dim / 2 pairs, with static YaRN when
+// yarn_factor > 1: the pair index where the number of rotations over the
+// original context, L f_i / (2 pi), equals n is d ln(L / (2 pi n)) /
+// (2 ln theta); pairs before the beta_fast index (rounded down) keep f_i, pairs
+// after the beta_slow index (rounded up) take f_i / s, linear in the index in
+// between.  P is qsa_params or qsa_layer_params.
+template <class P>
+void inv_freq(const P* p, double* f) {
   const int half = p->rope_dim / 2;
   const double d = (double)p->rope_dim, s = p->yarn_factor;
   double lo = 0.0, hi = 1.0;
@@ -93,7 +99,8 @@ void inv_freq(const qsa_params* p, double* f) {
 }
 
 // YaRN's attention factor on the rotated dims (1 without YaRN).
-double rope_attn_factor(const qsa_params* p) {
+template <class P>
+double rope_attn_factor(const P* p) {
   return p->yarn_factor > 1.0 ? 0.1 * std::log(p->yarn_factor) + 1.0 : 1.0;
 }
 
@@ -183,6 +190,12 @@ const char* nvtx_name(int32_t id) {
     case QSA_KERNEL_KBAR: return "qsa.kbar";
     case QSA_KERNEL_VERIFY_EXPAND: return "qsa.verify_expand";
     case QSA_KERNEL_IDX_ROPE: return "qsa.idx_rope";
+    case QSA_KERNEL_NORM_ROPE: return "qsa.norm_rope";
+    case QSA_KERNEL_PAGED_APPEND: return "qsa.paged_append";
+    case QSA_KERNEL_PAGED_DECODE: return "qsa.paged_decode";
+    case QSA_KERNEL_PAGED_DECODE_JOIN: return "qsa.paged_decode_join";
+    case QSA_KERNEL_PAGED_PREFILL: return "qsa.paged_prefill";
+    case QSA_KERNEL_PAGED_PREFILL_JOIN: return "qsa.paged_prefill_join";
     default: return "qsa.other";
   }
 }
@@ -1068,3 +1081,275 @@ qsa_status qsa_verify(const qsa_params* p, int32_t B, int32_t m, int64_t max_len
     return qsa::launch_decode_combine(rows, part_o, part_lse, cntt, n_split, out, lse_out, s);
   }));
 }
+
+// ------------------------------------------------- layers over a paged cache
+namespace {
+
+constexpr int32_t MAX_PAGED_B = 4096;
+
+qsa_status check_layer(const qsa_layer_params* p) {
+  if (!p) return QSA_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256) return QSA_ERR_UNSUPPORTED;
+  if (p->dtype != QSA_DTYPE_BF16 && p->dtype != QSA_DTYPE_FP16) return QSA_ERR_UNSUPPORTED;
+  if (p->n_q_heads <= 0 || p->n_kv_heads <= 0 || p->n_q_heads % p->n_kv_heads != 0) return QSA_ERR_INVALID_ARG;
+  if (p->n_q_heads > 1024 || p->n_q_heads / p->n_kv_heads > 64) return QSA_ERR_UNSUPPORTED;
+  if (p->rope_dim < 0) return QSA_ERR_INVALID_ARG;
+  if (p->rope_dim % 16 != 0 || p->rope_dim > p->head_dim) return QSA_ERR_UNSUPPORTED;
+  if (p->rope_axes != 1 && p->rope_axes != 3) return QSA_ERR_UNSUPPORTED;
+  if (p->rope_interleaved != 0 && p->rope_interleaved != 1) return QSA_ERR_INVALID_ARG;
+  if (p->rope_dim > 0) {
+    if (!(p->rope_theta > 1.0) || !std::isfinite(p->rope_theta) || !yarn_ok(p)) return QSA_ERR_INVALID_ARG;
+    if (p->rope_axes == 3) {
+      const int half = p->rope_dim / 2;
+      const int32_t* n = p->rope_section;
+      for (int a = 0; a < 3; ++a)
+        if (n[a] < 0 || n[a] > half) return QSA_ERR_INVALID_ARG;
+      if (n[0] + n[1] + n[2] != half) return QSA_ERR_INVALID_ARG;
+      // interleaved: the last pair of height (3 n - 2) and of width (3 n - 1) exists
+      if (p->rope_interleaved && ((n[1] > 0 && 3 * n[1] - 2 >= half) || (n[2] > 0 && 3 * n[2] - 1 >= half)))
+        return QSA_ERR_INVALID_ARG;
+    }
+  }
+  if (!(p->norm_eps > 0.f) || !std::isfinite(p->norm_eps)) return QSA_ERR_INVALID_ARG;
+  if (p->norm_zero_centred != 0 && p->norm_zero_centred != 1) return QSA_ERR_INVALID_ARG;
+  if (!(p->softmax_scale >= 0.f) || !std::isfinite(p->softmax_scale)) return QSA_ERR_INVALID_ARG;
+  if (p->window < 0 || p->n_sinks < 0) return QSA_ERR_INVALID_ARG;
+  return QSA_OK;
+}
+
+// Stride of rows of `width` elements: at least their width, whole 16-byte units.
+bool stride_ok(int64_t ld, int64_t width) { return ld >= width && ld % 8 == 0; }
+
+qsa_status check_kv(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B, qsa::PagedView* out) {
+  if (!kv || !kv->k_pages || !kv->v_pages || !kv->page_table) return QSA_ERR_INVALID_ARG;
+  if (!aligned16(kv->k_pages) || !aligned16(kv->v_pages)) return QSA_ERR_MISALIGNED;
+  if (kv->n_pages <= 0 || kv->page_size <= 0 || kv->max_pages <= 0 || kv->table_ld < kv->max_pages)
+    return QSA_ERR_INVALID_ARG;
+  if (kv->n_pages > INT32_MAX || kv->page_size > 65536) return QSA_ERR_UNSUPPORTED;
+  if (!stride_ok(kv->page_stride, p->head_dim) || !stride_ok(kv->token_stride, p->head_dim) ||
+      !stride_ok(kv->head_stride, p->head_dim))
+    return QSA_ERR_INVALID_ARG;
+  if (B <= 0) return QSA_ERR_INVALID_ARG;
+  if (B > MAX_PAGED_B) return QSA_ERR_UNSUPPORTED;
+  const int64_t cap = (int64_t)kv->max_pages * kv->page_size;
+  qsa::PagedView& v = *out;
+  v.k = static_cast<uint16_t*>(kv->k_pages);
+  v.v = static_cast<uint16_t*>(kv->v_pages);
+  v.page_stride = kv->page_stride;
+  v.token_stride = kv->token_stride;
+  v.head_stride = kv->head_stride;
+  v.table = kv->page_table;
+  v.table_ld = kv->table_ld;
+  v.n_pages = (int32_t)kv->n_pages;
+  v.page_size = kv->page_size;
+  v.capacity = (int32_t)std::min<int64_t>(cap, INT32_MAX);
+  // division by page_size: shift s with 2^s >= page_size, multiplier
+  // floor(2^32 (2^s - page_size) / page_size) + 1
+  uint32_t sh = 0;
+  while (((int64_t)1 << sh) < kv->page_size) ++sh;
+  v.div_shift = sh;
+  v.div_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << sh) - (uint64_t)kv->page_size)) /
+                             (uint64_t)kv->page_size + 1);
+  return QSA_OK;
+}
+
+void fill_rope(const qsa_layer_params* p, qsa::RopeSpec* r) {
+  const int half = p->rope_dim / 2;
+  r->half = half;
+  r->eps = p->norm_eps;
+  r->w_plus = p->norm_zero_centred ? 1.f : 0.f;
+  r->factor = 1.f;
+  if (half == 0) return;
+  inv_freq(p, r->f);
+  r->factor = (float)rope_attn_factor(p);
+  const int32_t* n = p->rope_section;
+  for (int i = 0; i < half; ++i) {
+    r->f[i] /= 3.14159265358979323846;
+    int a = 0;
+    if (p->rope_axes == 3) {
+      if (p->rope_interleaved) a = i % 3 != 0 && i < 3 * n[i % 3] ? i % 3 : 0;
+      else a = i < n[0] ? 0 : (i < n[0] + n[1] ? 1 : 2);
+    }
+    r->axis[i] = (uint8_t)a;
+  }
+}
+
+size_t paged_ws(const qsa_layer_params* p, int32_t B) {
+  return HEADER_BYTES +
+         align_up(std::max(qsa::paged_decode_scratch(p->head_dim, B), qsa::paged_prefill_scratch(p->head_dim)));
+}
+
+float layer_scale_log2(const qsa_layer_params* p) {
+  const float s = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)p->head_dim);
+  return s * 1.4426950408889634f;
+}
+
+}  // namespace
+
+extern "C" {
+
+void qsa_default_layer_params(qsa_layer_params* p) {
+  if (!p) return;
+  p->n_q_heads = 24;
+  p->n_kv_heads = 2;
+  p->head_dim = 256;
+  p->dtype = QSA_DTYPE_BF16;
+  p->rope_dim = 64;
+  p->rope_axes = 1;
+  p->rope_section[0] = 11;
+  p->rope_section[1] = 11;
+  p->rope_section[2] = 10;
+  p->rope_interleaved = 1;
+  p->rope_theta = 1e7;
+  p->yarn_factor = 0.0;
+  p->yarn_original_max = 262144.0;
+  p->yarn_beta_fast = 32.0;
+  p->yarn_beta_slow = 1.0;
+  p->norm_eps = 1e-6f;
+  p->norm_zero_centred = 1;
+  p->softmax_scale = 0.f;
+  p->window = 0;
+  p->n_sinks = 0;
+}
+
+qsa_status qsa_norm_rope(const qsa_layer_params* p, int64_t T, int64_t pos0, const int32_t* positions, const void* q,
+                         int64_t q_ld, const void* k, int64_t k_ld, const void* q_weight, const void* k_weight,
+                         void* q_out, void* k_out, void* stream) {
+  qsa_status st = check_layer(p);
+  if (st != QSA_OK) return st;
+  if (T < 0 || (!q != !q_out) || (!k != !k_out) || (!q && !k) || pos0 < 0) return QSA_ERR_INVALID_ARG;
+  if (T > INT32_MAX || pos0 > INT32_MAX) return QSA_ERR_UNSUPPORTED;
+  if ((q && !stride_ok(q_ld, (int64_t)p->n_q_heads * p->head_dim)) ||
+      (k && !stride_ok(k_ld, (int64_t)p->n_kv_heads * p->head_dim)))
+    return QSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(q_out) ||
+      !aligned16(k_out))
+    return QSA_ERR_MISALIGNED;
+  DevInfo di;
+  if ((st = device_info(&di)) != QSA_OK) return st;
+  if (T == 0) return QSA_OK;
+  qsa::NormRopeArgs a{};
+  a.T = T; a.pos0 = pos0; a.positions = positions;
+  a.q = static_cast<const uint16_t*>(q); a.q_ld = q_ld;
+  a.k = static_cast<const uint16_t*>(k); a.k_ld = k_ld;
+  a.q_weight = static_cast<const uint16_t*>(q_weight);
+  a.k_weight = static_cast<const uint16_t*>(k_weight);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.hq = p->n_q_heads; a.hk = p->n_kv_heads;
+  fill_rope(p, &a.rope);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return from_cuda(traced(QSA_KERNEL_NORM_ROPE, s, [&] {
+    return qsa::launch_norm_rope(a, p->head_dim, p->dtype, false, s);
+  }), "norm and rotation launch");
+}
+
+qsa_status qsa_paged_workspace_size(const qsa_layer_params* p, int32_t B, int64_t T, size_t* bytes) {
+  qsa_status st = check_layer(p);
+  if (st != QSA_OK) return st;
+  if (!bytes || B <= 0 || T < 0) return QSA_ERR_INVALID_ARG;
+  if (B > MAX_PAGED_B || T >= ((int64_t)1 << 24)) return QSA_ERR_UNSUPPORTED;
+  *bytes = paged_ws(p, B);
+  return QSA_OK;
+}
+
+qsa_status qsa_paged_append(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B, int64_t T,
+                            const int32_t* cu_new, const int32_t* cache_len, const int32_t* positions, const void* q,
+                            int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                            const void* q_weight, const void* k_weight, void* q_out, void* ws, size_t ws_bytes,
+                            void* stream) {
+  qsa_status st = check_layer(p);
+  if (st != QSA_OK) return st;
+  qsa::NormRopeArgs a{};
+  if ((st = check_kv(p, kv, B, &a.kv)) != QSA_OK) return st;
+  if (T < 0 || !cache_len || !k || !v || !ws || (!q != !q_out) || (!cu_new && T != B)) return QSA_ERR_INVALID_ARG;
+  if (T >= ((int64_t)1 << 24)) return QSA_ERR_UNSUPPORTED;
+  const int64_t kw = (int64_t)p->n_kv_heads * p->head_dim;
+  if ((q && !stride_ok(q_ld, (int64_t)p->n_q_heads * p->head_dim)) || !stride_ok(k_ld, kw) || !stride_ok(v_ld, kw))
+    return QSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_weight) || !aligned16(k_weight) ||
+      !aligned16(q_out) || !aligned16(ws))
+    return QSA_ERR_MISALIGNED;
+  if (ws_bytes < HEADER_BYTES) return QSA_ERR_WORKSPACE_TOO_SMALL;
+  DevInfo di;
+  if ((st = device_info(&di)) != QSA_OK) return st;
+  if (T == 0) return QSA_OK;
+  a.T = T; a.positions = positions;
+  a.q = static_cast<const uint16_t*>(q); a.q_ld = q_ld;
+  a.k = static_cast<const uint16_t*>(k); a.k_ld = k_ld;
+  a.v = static_cast<const uint16_t*>(v); a.v_ld = v_ld;
+  a.q_weight = static_cast<const uint16_t*>(q_weight);
+  a.k_weight = static_cast<const uint16_t*>(k_weight);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.hq = p->n_q_heads; a.hk = p->n_kv_heads;
+  a.B = B; a.cu_new = cu_new; a.cache_len = cache_len;
+  a.err = static_cast<uint32_t*>(ws);
+  fill_rope(p, &a.rope);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return from_cuda(traced(QSA_KERNEL_PAGED_APPEND, s, [&] {
+    return qsa::launch_norm_rope(a, p->head_dim, p->dtype, true, s);
+  }), "paged append launch");
+}
+
+qsa_status qsa_paged_decode(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B, const int32_t* cache_len,
+                            const void* q, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  qsa_status st = check_layer(p);
+  if (st != QSA_OK) return st;
+  qsa::PagedAttnArgs a{};
+  if ((st = check_kv(p, kv, B, &a.kv)) != QSA_OK) return st;
+  if (!cache_len || !q || !out || !ws) return QSA_ERR_INVALID_ARG;
+  if ((int64_t)B * a.kv.capacity > ((int64_t)1 << 36)) return QSA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(ws)) return QSA_ERR_MISALIGNED;
+  if (ws_bytes < paged_ws(p, B)) return QSA_ERR_WORKSPACE_TOO_SMALL;
+  DevInfo di;
+  if ((st = device_info(&di)) != QSA_OK) return st;
+  a.B = B; a.hq = p->n_q_heads; a.hk = p->n_kv_heads; a.T = B;
+  a.cache_len = cache_len;
+  a.q = static_cast<const uint16_t*>(q);
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.scale_log2 = layer_scale_log2(p);
+  a.window = p->window; a.sinks = p->n_sinks;
+  a.err = static_cast<uint32_t*>(ws);
+  a.scratch = static_cast<uint8_t*>(ws) + HEADER_BYTES;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = from_cuda(traced(QSA_KERNEL_PAGED_DECODE, s, [&] {
+         return qsa::launch_paged_decode(a, p->head_dim, p->dtype, di.num_sms, s, false);
+       }), "paged decode launch")) != QSA_OK)
+    return st;
+  return from_cuda(traced(QSA_KERNEL_PAGED_DECODE_JOIN, s, [&] {
+    return qsa::launch_paged_decode(a, p->head_dim, p->dtype, di.num_sms, s, true);
+  }), "paged decode join launch");
+}
+
+qsa_status qsa_paged_prefill(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B, int64_t T,
+                             const int32_t* cu_new, const int32_t* cache_len, const void* q, void* out, float* lse,
+                             void* ws, size_t ws_bytes, void* stream) {
+  qsa_status st = check_layer(p);
+  if (st != QSA_OK) return st;
+  qsa::PagedAttnArgs a{};
+  if ((st = check_kv(p, kv, B, &a.kv)) != QSA_OK) return st;
+  if (T < 0 || !cu_new || !cache_len || !q || !out || !ws) return QSA_ERR_INVALID_ARG;
+  if (T >= ((int64_t)1 << 24)) return QSA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(ws)) return QSA_ERR_MISALIGNED;
+  if (ws_bytes < paged_ws(p, B)) return QSA_ERR_WORKSPACE_TOO_SMALL;
+  DevInfo di;
+  if ((st = device_info(&di)) != QSA_OK) return st;
+  if (T == 0) return QSA_OK;
+  a.B = B; a.hq = p->n_q_heads; a.hk = p->n_kv_heads; a.T = T;
+  a.cu_new = cu_new;
+  a.cache_len = cache_len;
+  a.q = static_cast<const uint16_t*>(q);
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.scale_log2 = layer_scale_log2(p);
+  a.window = p->window; a.sinks = p->n_sinks;
+  a.err = static_cast<uint32_t*>(ws);
+  a.scratch = static_cast<uint8_t*>(ws) + HEADER_BYTES;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return from_cuda(traced(QSA_KERNEL_PAGED_PREFILL, s, [&] {
+    return qsa::launch_paged_prefill(a, p->head_dim, p->dtype, di.num_sms, s, false);
+  }), "paged prefill launch");
+}
+
+}  // extern "C"

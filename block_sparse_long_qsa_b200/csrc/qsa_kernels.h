@@ -119,4 +119,67 @@ cudaError_t launch_verify_expand(int B, int m, int nqv, int budget, const int64_
 cudaError_t launch_decode_combine(int B, const float* part_o, const float* part_lse, const int32_t* cnt, int n_split,
                                   uint16_t* out, float* lse, cudaStream_t stream);
 
+// ------------------------------------------------------------ paged cache
+// qsa_paged_kv as the kernels take it.
+struct PagedView {
+  uint16_t* k;
+  uint16_t* v;
+  int64_t page_stride, token_stride, head_stride;   // elements
+  const int32_t* table;
+  int64_t table_ld;
+  int32_t n_pages;
+  int32_t page_size;
+  uint32_t div_mul, div_shift;                      // j / page_size (page_of)
+  int32_t capacity;                                 // tokens a table row can hold
+};
+
+// Rotation and norm of qsa_layer_params.
+struct RopeSpec {
+  double f[128];            // frequency of each pair over pi (angles in half turns)
+  uint8_t axis[128];        // position axis of each pair
+  float factor;             // on the rotated dims (YaRN)
+  int half;                 // rope_dim / 2
+  float eps, w_plus;        // norm: epsilon, what is added to the weights (0 or 1)
+};
+
+// Norm and rotation of q and k heads (qsa_norm_rope), and the append
+// (qsa_paged_append: kv non-null, k rows go to the pages and v beside them).
+struct NormRopeArgs {
+  int64_t T, pos0;
+  const int32_t* positions; // [axes][T] or null
+  const uint16_t* q; const uint16_t* k; const uint16_t* v;
+  int64_t q_ld, k_ld, v_ld;
+  const uint16_t* q_weight; const uint16_t* k_weight;
+  uint16_t* q_out; uint16_t* k_out;
+  int hq, hk;
+  // append
+  int B;
+  const int32_t* cu_new; const int32_t* cache_len;
+  PagedView kv;
+  uint32_t* err;
+  RopeSpec rope;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int head_dim, int dtype, bool append, cudaStream_t s);
+
+struct PagedAttnArgs {
+  PagedView kv;
+  int B, hq, hk;
+  int64_t T;                // rows of q / out
+  const int32_t* cu_new;    // prefill
+  const int32_t* cache_len;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  float scale_log2;
+  int window, sinks;
+  uint32_t* err;
+  void* scratch;            // behind the workspace's header
+};
+size_t paged_decode_scratch(int head_dim, int B);
+cudaError_t launch_paged_decode(const PagedAttnArgs& a, int head_dim, int dtype, int num_sms, cudaStream_t s,
+                                bool join);
+size_t paged_prefill_scratch(int head_dim);
+cudaError_t launch_paged_prefill(const PagedAttnArgs& a, int head_dim, int dtype, int num_sms, cudaStream_t s,
+                                 bool join);
+
 }  // namespace qsa

@@ -12,6 +12,8 @@
  *      block, always including the query block itself and the one before it;
  *   3. GQA softmax attention (24 Q heads, 2 KV heads, head dim 256, RoPE with
  *      theta = 1e7 on dims 0..63) runs over the selected blocks only.
+ * Beside it, the operators of dense and sliding-window layers over a paged
+ * cache (qsa_norm_rope, qsa_paged_*).
  *
  * Conventions (all calls):
  *   - Every pointer argument is a DEVICE pointer unless marked "host", 16-byte
@@ -351,9 +353,164 @@ qsa_status qsa_decode_noalloc(const qsa_params* p, int32_t B, int64_t max_len, c
  * clears the word when it starts), then clears it. */
 qsa_status qsa_decode_noalloc_check_error(void* stream);
 
+/* ---- Layers over a paged KV cache ------------------------------------------
+ * The dense and sliding-window attention layers of a model that also runs QSA
+ * layers, served from a paged cache: the norms of query and key heads with the
+ * rotation of positions ([PT] spec: zero-centred RMSNorm; rope_parameters
+ * listing: mrope_interleaved, sections [11, 11, 10]), the append of new tokens
+ * to the pages, the attention of one new token per sequence, and the attention
+ * of a ragged batch of new tokens (prompts, chunks of prompts, verify steps).
+ *
+ * Conventions of these calls, beside those above:
+ *   - Elements are 16-bit, bf16 or fp16 by qsa_layer_params.dtype, as bit
+ *     patterns.  Sums, statistics and rotations are fp32 (angles are formed in
+ *     fp64), each result is rounded to the element type once.
+ *   - Lengths, offsets, positions and page tables are DEVICE int32 arrays, read
+ *     when the call runs: a captured graph follows lengths that change between
+ *     replays.  They need 4-byte alignment only.
+ *   - Sequence b has cache_len[b] tokens in its cache before the call's tokens;
+ *     its new token i has cache position cache_len[b] + i.  cache_len[b] < 0
+ *     marks a padding sequence: nothing of it is read or written.
+ *   - Ragged batches: sequence b's new tokens are rows cu_new[b] ..
+ *     cu_new[b + 1] - 1 of the token arrays (cu_new: B + 1 ascending offsets,
+ *     0 <= cu_new[b] <= T).  Rows outside [cu_new[0], cu_new[B]) are left as
+ *     they were.
+ *   - Workspace: qsa_paged_workspace_size bytes.  These calls do not clear the
+ *     error word at its start: call qsa_check_device_error on the workspace
+ *     once after allocating it (it clears the word), then any number of calls
+ *     may share it, one after another, and the word keeps the first error
+ *     until the next qsa_check_device_error.  Calls that overlap on the GPU
+ *     need a workspace each.
+ *   - Device-side checks: a page id outside [0, n_pages), and a position past
+ *     the table, record QSA_ERR_DEVICE_BOUNDS; the tokens there are left out
+ *     (not written by the append, masked in the attention).  Only entries of
+ *     pages that hold a needed token are read, so entries of pages given back
+ *     behind a window may hold anything. */
+enum { QSA_DTYPE_BF16 = 0, QSA_DTYPE_FP16 = 1 };
+
+/* Shape and numerics of one such layer.  Accepted: head_dim 64, 128 or 256;
+ * n_q_heads a multiple of n_kv_heads, at most 64 query heads to a KV head and
+ * 1024 in all (query head h reads KV head h / (n_q_heads / n_kv_heads));
+ * rope_dim 0 (no rotation) or a multiple of 16 up to head_dim. */
+typedef struct {
+  int32_t n_q_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t dtype;            /* QSA_DTYPE_* */
+  /* Rotation of dims 0 .. rope_dim-1, pairs (i, i + rope_dim/2), angle =
+   * position * f_i, f_i = rope_theta^(-2i/rope_dim), with static YaRN as in
+   * qsa_params (yarn_factor <= 1: plain). */
+  int32_t rope_dim;
+  /* rope_axes 1: one position per token.  3: positions of time, height and
+   * width; rope_section[a] of the rope_dim/2 pairs turn by axis a (their sum
+   * is rope_dim/2).  rope_interleaved 1: pair i turns by axis i % 3 while i <
+   * 3 * rope_section[i % 3] (height and width), all other pairs by time.  0:
+   * the first rope_section[0] pairs turn by time, the next by height, the
+   * rest by width. */
+  int32_t rope_axes;
+  int32_t rope_section[3];
+  int32_t rope_interleaved;
+  double rope_theta;
+  double yarn_factor;
+  double yarn_original_max;
+  double yarn_beta_fast;
+  double yarn_beta_slow;
+  /* RMS norm: y = x / sqrt(mean(x^2) + norm_eps) * w, with w + 1 for w when
+   * norm_zero_centred is 1.  Domain: |x| < 2^60 (squares are summed in fp32). */
+  float norm_eps;           /* > 0 */
+  int32_t norm_zero_centred;
+  float softmax_scale;      /* 0: 1 / sqrt(head_dim) */
+  /* window W > 0: the token at position i sees keys i-W+1 .. i and the first
+   * n_sinks keys.  window 0: all keys up to its own (n_sinks without effect). */
+  int32_t window;
+  int32_t n_sinks;
+} qsa_layer_params;
+
+/* 24 query and 2 KV heads of 256 dims, bf16, rope_dim 64, one axis (sections
+ * 11, 11, 10, interleaved, for rope_axes = 3), theta 1e7, no YaRN, norm_eps
+ * 1e-6, zero-centred, default scale, no window. */
+void qsa_default_layer_params(qsa_layer_params* p);
+
+/* A paged cache.  Token j of sequence b is in page page_table[b * table_ld +
+ * j / page_size], slot j % page_size; its row of KV head g starts at element
+ *   page * page_stride + slot * token_stride + g * head_stride
+ * of k_pages and of v_pages.  Strides are in elements, multiples of 8, at least
+ * head_dim; both pointers are 16-byte aligned.  So token-major pages
+ * [n_pages][page_size][n_kv][head_dim], head-major ones, and pages that hold K
+ * and V side by side all fit.  page_size: any, 1 .. 65536.  Pages may be shared
+ * by sequences as long as no call appends to a shared page. */
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  int64_t n_pages;          /* < 2^31 */
+  int32_t page_size;
+  int32_t max_pages;        /* entries of a table row */
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  const int32_t* page_table;
+  int64_t table_ld;         /* entries between rows, >= max_pages */
+} qsa_paged_kv;
+
+/* Norm and rotation of T tokens' query and key heads in one pass:
+ *   q_out[t][h] = rotate(norm(q[t][h], q_weight)), k_out alike.
+ * q: row t at q + t * q_ld elements, [n_q_heads][head_dim] inside; k alike with
+ * k_ld (so both may be slices of one projection's output; q_ld, k_ld multiples
+ * of 8).  q_weight, k_weight [head_dim] of the element type; NULL: that norm is
+ * left out.  positions [rope_axes][T] int32 (device); NULL: pos0 + t on every
+ * axis.  q_out [T][n_q_heads][head_dim], k_out [T][n_kv_heads][head_dim].  q
+ * with q_out, or k with k_out, may be NULL.  q_out may be q itself when q_ld is
+ * n_q_heads * head_dim (k alike); otherwise outputs overlap no input.
+ * With rope_dim 0 the outputs feed qsa_prefill and qsa_decode, which rotate
+ * by themselves. */
+qsa_status qsa_norm_rope(const qsa_layer_params* p, int64_t T, int64_t pos0, const int32_t* positions, const void* q,
+                         int64_t q_ld, const void* k, int64_t k_ld, const void* q_weight, const void* k_weight,
+                         void* q_out, void* k_out, void* stream);
+
+/* Append of T new tokens of B sequences: k normed and rotated as by
+ * qsa_norm_rope, v as it is, both into the pages at cache positions
+ * cache_len[b] + i; with q (nullable, with q_out) the queries normed and rotated
+ * in the same launch.  cu_new NULL: one token per sequence (T == B).  positions
+ * NULL: the cache position on every axis.  k, v rows at k_ld, v_ld (multiples
+ * of 8); weights, positions and q as above.  The caller advances cache_len.
+ * Reads and writes each element once. */
+qsa_status qsa_paged_append(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B, int64_t T,
+                            const int32_t* cu_new, const int32_t* cache_len, const int32_t* positions, const void* q,
+                            int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                            const void* q_weight, const void* k_weight, void* q_out, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Attention of one new token per sequence over its pages, the token itself (at
+ * position cache_len[b], already appended) included:
+ *   out[b][h] = sum_j softmax_j(q[b][h] . k[j] * scale) v[j],
+ *   lse[b][h] = log sum_j exp(q[b][h] . k[j] * scale)   (nullable),
+ * over the keys j <= cache_len[b] that window and sinks leave.  q, out
+ * [B][n_q_heads][head_dim]; lse fp32 [B][n_q_heads].  Rows of padding sequences
+ * are left as they were; a row all of whose keys lie on bad pages is zero, its
+ * lse -inf.  Slots of masked or absent tokens are not read (they may hold NaN).
+ * The keys of all sequences and KV heads are cut evenly over the SMs; partial
+ * results are joined by their log-sum-exp in a fixed order.
+ * B <= 4096, B * max_pages * page_size <= 2^36. */
+qsa_status qsa_paged_decode(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B, const int32_t* cache_len,
+                            const void* q, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of T new tokens of B sequences (ragged, cu_new) over their pages:
+ * every token sees the keys up to its own position that window and sinks leave,
+ * cached ones and the call's own (already appended).  q, out
+ * [T][n_q_heads][head_dim], lse [T][n_q_heads] (nullable).  What the pages hold
+ * behind a sequence's last token is not read; a V row that is not finite
+ * reaches only the tokens that see it and, within its tile of 128 keys, may turn
+ * rows of earlier tokens of the same call into NaN.  B <= 4096, T < 2^24. */
+qsa_status qsa_paged_prefill(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B, int64_t T,
+                             const int32_t* cu_new, const int32_t* cache_len, const void* q, void* out, float* lse,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace of the paged calls for up to B sequences and T new tokens. */
+qsa_status qsa_paged_workspace_size(const qsa_layer_params* p, int32_t B, int64_t T, size_t* bytes);
+
 /* Reads (synchronising `stream`) and clears the device error word at the
  * start of a workspace passed to qsa_select_blocks / qsa_prefill /
- * qsa_decode.  Returns QSA_OK or the first device-side error recorded. */
+ * qsa_decode or to the paged calls.  Returns QSA_OK or the first device-side error recorded. */
 qsa_status qsa_check_device_error(void* ws, void* stream);
 
 /* Launch tracing, a measurement aid with no counterpart on the pages.
@@ -376,7 +533,13 @@ enum {
   QSA_KERNEL_DECODE_COMBINE = 9,
   QSA_KERNEL_KBAR = 10,
   QSA_KERNEL_VERIFY_EXPAND = 11,
-  QSA_KERNEL_IDX_ROPE = 12
+  QSA_KERNEL_IDX_ROPE = 12,
+  QSA_KERNEL_NORM_ROPE = 13,
+  QSA_KERNEL_PAGED_APPEND = 14,
+  QSA_KERNEL_PAGED_DECODE = 15,
+  QSA_KERNEL_PAGED_DECODE_JOIN = 16,
+  QSA_KERNEL_PAGED_PREFILL = 17,
+  QSA_KERNEL_PAGED_PREFILL_JOIN = 18
 };
 qsa_status qsa_trace_begin(int32_t capacity);
 qsa_status qsa_trace_end(int32_t* kernel_ids, float* ms, int32_t capacity, int32_t* n_out);

@@ -1,0 +1,541 @@
+"""The paged-cache calls on the GPU against 64-bit references: norms and
+rotation, append, decode, prefill, and a run of them as a server makes it."""
+import pytest
+import torch
+
+import block_sparse_long_qsa_b200 as qsa
+import paged_util as U
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+HEADS = [(24, 2, 256), (7, 7, 128), (28, 4, 128), (16, 16, 64), (40, 1, 64), (64, 1, 128), (17, 1, 256)]
+
+
+def randn(g, dt, *shape):
+    return torch.randn(shape, generator=g, dtype=torch.float32).to(dt).cuda()
+
+
+def gen(seed=0):
+    return torch.Generator().manual_seed(seed)
+
+
+def ok(ws):
+    torch.cuda.synchronize()
+    return qsa.qsa_check_device_error(ws)
+
+
+# ------------------------------------------------------------- norm and rotation
+@pytest.mark.parametrize("T", [1, 2, 5, 67])
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("heads,rope", [((24, 2, 256), 64), ((7, 7, 128), 128), ((16, 16, 64), 32), ((40, 1, 64), 64),
+                                        ((24, 2, 256), 256), ((28, 4, 128), 16), ((3, 3, 128), 0)])
+def test_norm_rope(heads, rope, dt, T):
+    hq, hk, D = heads
+    g = gen(T)
+    p = qsa.layer_params(hq, hk, D, dtype=dt, rope_dim=rope)
+    qkv = randn(g, dt, T, hq + 2 * hk, D)
+    q, k = qkv[:, :hq], qkv[:, hq:hq + hk]
+    qw, kw = randn(g, dt, D), randn(g, dt, D)
+    qo, ko = torch.empty(T, hq, D, dtype=dt, device="cuda"), torch.empty(T, hk, D, dtype=dt, device="cuda")
+    qsa.qsa_norm_rope(p, T, 1000003, q, k, qw, kw, qo, ko)
+    pos = 1000003 + torch.arange(T, device="cuda")[None]
+    for got, x, w in ((qo, q, qw), (ko, k, kw)):
+        U.check_norm_rope(got, *U.norm_rope64(p, x, w, pos), dt)
+
+
+@pytest.mark.parametrize("rope,section", [(64, (11, 11, 10)), (64, (16, 8, 8)), (128, (24, 20, 20)), (32, (16, 0, 0)), (64, (21, 0, 11))])
+@pytest.mark.parametrize("interleaved", [0, 1])
+def test_three_axes(rope, section, interleaved):
+    if interleaved and section == (21, 0, 11):
+        section = (22, 0, 10)
+    T, hq, hk, D = 33, 4, 2, 128
+    g = gen(3)
+    p = qsa.layer_params(hq, hk, D, rope_dim=rope, rope_axes=3, rope_section=section, rope_interleaved=interleaved)
+    q, k, qw = randn(g, BF, T, hq, D), randn(g, BF, T, hk, D), randn(g, BF, D)
+    pos = torch.randint(0, 1 << 21, (3, T), generator=g, dtype=torch.int32).cuda()
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    qsa.qsa_norm_rope(p, T, 0, q, k, qw, None, qo, ko, positions=pos)
+    U.check_norm_rope(qo, *U.norm_rope64(p, q, qw, pos), BF)
+    U.check_norm_rope(ko, *U.norm_rope64(p, k, None, pos), BF)         # no weight: no norm
+    one = qsa.layer_params(hq, hk, D, rope_dim=rope)                   # a text token: one position on all axes
+    same = torch.arange(T, dtype=torch.int32, device="cuda").expand(3, T).contiguous()
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    qsa.qsa_norm_rope(p, T, 0, q, None, qw, None, a, None, positions=same)
+    qsa.qsa_norm_rope(one, T, 0, q, None, qw, None, b, None)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("centred", [0, 1])
+@pytest.mark.parametrize("pos0", [0, (1 << 31) - 10])
+def test_norm_rope_yarn_and_far_positions(pos0, centred):
+    T, hq, hk, D = 9, 6, 2, 256
+    g = gen(5)
+    p = qsa.layer_params(hq, hk, D, rope_dim=64, yarn_factor=4.0, norm_zero_centred=centred, norm_eps=1e-3)
+    k, kw = randn(g, BF, T, hk, D) * 1e-2, randn(g, BF, D)
+    ko = torch.empty_like(k)
+    qsa.qsa_norm_rope(p, T, pos0, None, k, None, kw, None, ko)
+    pos = (pos0 + torch.arange(T, device="cuda"))[None]
+    U.check_norm_rope(ko, *U.norm_rope64(p, k, kw, pos), BF)
+
+
+def test_norm_rope_in_place_and_rows_behind():
+    T, hq, hk, D = 11, 24, 2, 256
+    g = gen(6)
+    p = qsa.layer_params(hq, hk, D)
+    q, k, w = randn(g, BF, T + 3, hq, D), randn(g, BF, T + 3, hk, D), randn(g, BF, D)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    qsa.qsa_norm_rope(p, T, 7, q, k, w, w, qo, ko)
+    q2, k2 = q.clone(), k.clone()
+    qsa.qsa_norm_rope(p, T, 7, q2, k2, w, w, q2, k2)
+    assert torch.equal(q2[:T], qo[:T]) and torch.equal(k2[:T], ko[:T])
+    assert torch.equal(q2[T:], q[T:]) and torch.equal(k2[T:], k[T:])
+    qsa.qsa_norm_rope(p, 0, 7, q2, k2, w, w, q2, k2)                   # nothing to do
+    zero = torch.zeros(1, hq, D, dtype=BF, device="cuda")
+    qsa.qsa_norm_rope(p, 1, 7, zero, None, w, None, zero, None)        # eps keeps a zero row finite
+    assert torch.equal(zero, torch.zeros_like(zero))
+
+
+# ------------------------------------------------------------------------ append
+@pytest.mark.parametrize("layout", ["token", "head", "beside"])
+@pytest.mark.parametrize("page", [1, 3, 16, 48])
+@pytest.mark.parametrize("heads,dt", [((24, 2, 256), BF), ((7, 7, 128), FP), ((40, 1, 64), BF)])
+def test_append(heads, dt, page, layout):
+    hq, hk, D = heads
+    g = gen(page)
+    p = qsa.layer_params(hq, hk, D, dtype=dt, rope_dim=32)
+    cached, new = [0, 17, -1, 5, 40, 1], [3, 1, 4, 0, 33, 1]          # a padding and an empty sequence among them
+    lens = [max(c, 0) + n for c, n in zip(cached, new)]
+    cache = U.Cache(p, lens, page, dt, "cuda", layout)
+    B, T = len(new), sum(new) + 3                                      # three rows behind the last sequence
+    cu = torch.tensor([0] + list(torch.tensor(new).cumsum(0)), dtype=torch.int32, device="cuda")
+    cl = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    qkv = randn(g, dt, T, hq + 2 * hk, D)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+    qw, kw = randn(g, dt, D), randn(g, dt, D)
+    qo = torch.full((T, hq, D), 5.0, dtype=dt, device="cuda")
+    ws = qsa.paged_workspace(p, B, T)
+    qsa.qsa_paged_append(p, cache.kv, B, T, cu, cl, k, v, ws, q=q, q_out=qo, q_weight=qw, k_weight=kw)
+    assert ok(ws) == 0
+    written = torch.zeros(cache.k.shape[:2], dtype=torch.bool, device="cuda")
+    for b in range(B):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        if cached[b] < 0:
+            assert bool((qo[rows] == 5).all())
+            continue
+        at = cached[b] + torch.arange(new[b], device="cuda")
+        U.check_norm_rope(qo[rows], *U.norm_rope64(p, q[rows], qw, at[None]), dt)
+        pg, sl = cache.slots(b, at)
+        U.check_norm_rope(cache.k[pg, sl], *U.norm_rope64(p, k[rows], kw, at[None]), dt)
+        assert torch.equal(cache.v[pg, sl], v[rows])
+        written[pg, sl] = True
+    assert bool((qo[T - 3:] == 5).all())
+    assert bool(cache.k[~written].isnan().all()) and bool(cache.v[~written].isnan().all())
+
+
+def test_append_one_token_each_without_queries():
+    hq, hk, D, B = 8, 4, 128, 70
+    p = qsa.layer_params(hq, hk, D, rope_axes=3)
+    cached = [(b * 37) % 100 for b in range(B)]
+    cache = U.Cache(p, [c + 1 for c in cached], 16, BF, "cuda")
+    g = gen(9)
+    k, v, kw = randn(g, BF, B, hk, D), randn(g, BF, B, hk, D), randn(g, BF, D)
+    pos = torch.randint(0, 5000, (3, B), generator=g, dtype=torch.int32).cuda()
+    ws = qsa.paged_workspace(p, B, B)
+    cl = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    qsa.qsa_paged_append(p, cache.kv, B, B, None, cl, k, v, ws, k_weight=kw, positions=pos)
+    assert ok(ws) == 0
+    want, size = U.norm_rope64(p, k, kw, pos)
+    for b in range(B):
+        pg, sl = cache.slots(b, torch.tensor([cached[b]], device="cuda"))
+        U.check_norm_rope(cache.k[pg, sl], want[b:b + 1], size[b:b + 1], BF)
+        assert torch.equal(cache.v[pg, sl], v[b:b + 1])
+
+
+def test_append_bad_pages_are_left_out_and_reported():
+    p = qsa.layer_params(4, 2, 64, rope_dim=0)
+    cache = U.Cache(p, [8, 8, 8], 4, BF, "cuda")
+    cache.table[0, 1] = cache.k.shape[0]                               # one past the pool
+    cache.table[1, 1] = -1
+    g = gen(1)
+    k, v = randn(g, BF, 12, 2, 64), randn(g, BF, 12, 2, 64)
+    cu = torch.tensor([0, 4, 8, 12], dtype=torch.int32, device="cuda")
+    ws = qsa.paged_workspace(p, 3, 12)
+    for cl, good in [([2, 2, 2], [(0, 2), (1, 2), (2, 4)]), ([100, 0, 0], [(1, 4), (2, 4)])]:
+        cache.k.fill_(float("nan"))
+        cache.v.fill_(float("nan"))
+        qsa.qsa_paged_append(p, cache.kv, 3, 12, cu, torch.tensor(cl, dtype=torch.int32, device="cuda"), k, v, ws)
+        assert ok(ws) == 7                                             # QSA_ERR_DEVICE_BOUNDS, then cleared
+        assert ok(ws) == 0
+        assert int((~cache.k[..., 0].isnan()).sum()) == 2 * sum(n for _, n in good)
+        for b, n in good:
+            at = torch.arange(cl[b], cl[b] + n, device="cuda")
+            pg, sl = cache.slots(b, at)
+            assert torch.equal(cache.k[pg, sl], k[4 * b:4 * b + n]) and torch.equal(cache.v[pg, sl], v[4 * b:4 * b + n])
+
+
+# --------------------------------------------------------------------- attention
+def batch(p, cached, new, page, dt, layout="token", seed=0, spread=1.0):
+    """A cache that holds all tokens' keys and values, and the new tokens' queries."""
+    g = gen(seed)
+    needed = [U.needed_pages(p, c, c + n - 1, page) if c >= 0 and n else [] for c, n in zip(cached, new)]
+    lens = [max(c, 0) + n for c, n in zip(cached, new)]
+    cache = U.Cache(p, lens, page, dt, "cuda", layout, seed, needed=needed)
+    for b, need in enumerate(needed):
+        for j in need:
+            lo, hi = j * page, min((j + 1) * page, lens[b])
+            cache.fill(b, lo, hi, spread * randn(g, dt, hi - lo, p.n_kv_heads, p.head_dim),
+                       randn(g, dt, hi - lo, p.n_kv_heads, p.head_dim))
+    q = randn(g, dt, sum(new), p.n_q_heads, p.head_dim)
+    cl = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0] + list(torch.tensor(new).cumsum(0)), dtype=torch.int32, device="cuda")
+    return cache, q, cl, cu
+
+
+def check_batch(p, cache, cached, new, q, out, lse, dt, tokens=None):
+    row = 0
+    for b, (c, n) in enumerate(zip(cached, new)):
+        for i in range(n):
+            if c >= 0 and (tokens is None or i in tokens(n)):
+                keys = U.visible(p, c + i).cuda()
+                k, v = cache.rows(b, keys)
+                U.check_row(out[row + i], None if lse is None else lse[row + i], U.attend64(p, q[row + i], k, v), dt)
+        row += n
+
+
+def run_decode(p, cache, q, cl, ws=None):
+    B = q.shape[0]
+    out = torch.full_like(q, 9.0)
+    lse = torch.full(q.shape[:2], 9.0, dtype=torch.float32, device="cuda")
+    ws = qsa.paged_workspace(p, B, B) if ws is None else ws
+    qsa.qsa_paged_decode(p, cache.kv, B, cl, q, out, ws, lse=lse)
+    return out, lse, ws
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("dt,page,layout", [(BF, 16, "token"), (FP, 48, "head"), (BF, 1, "beside")])
+def test_decode(heads, dt, page, layout):
+    p = qsa.layer_params(*heads, dtype=dt)
+    cached = [0, 1, 14, 15, 16, 63, 64, 200, 1025, -1, 511]
+    cache, q, cl, _ = batch(p, cached, [1] * len(cached), page, dt, layout)
+    out, lse, ws = run_decode(p, cache, q, cl)
+    assert ok(ws) == 0
+    check_batch(p, cache, cached, [1] * len(cached), q, out, lse, dt)
+    assert bool((out[9] == 9).all()) and bool((lse[9] == 9).all())     # padding: left as it was
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (100, 0), (100, 64), (100, 300), (4096, 4)])
+@pytest.mark.parametrize("heads", [(24, 2, 256), (28, 4, 128), (16, 16, 64)])
+def test_decode_window(heads, window, sinks):
+    """Pages that hold no visible key have no entry in the table."""
+    p = qsa.layer_params(*heads, window=window, n_sinks=sinks)
+    cached = [0, 1, window - 1, window, window + 1, window + sinks, window + sinks + 1, 3 * window + 517, 5000]
+    cache, q, cl, _ = batch(p, cached, [1] * len(cached), 16, BF, seed=window)
+    out, lse, ws = run_decode(p, cache, q, cl)
+    assert ok(ws) == 0
+    check_batch(p, cache, cached, [1] * len(cached), q, out, lse, BF)
+
+
+@pytest.mark.parametrize("heads", [(24, 2, 256), (7, 7, 128)])
+def test_decode_one_long_sequence_and_many_short(heads):
+    """Both ends of the split: one sequence over all SMs, and many to an SM."""
+    p = qsa.layer_params(*heads)
+    for cached in ([20011], [(b * 29) % 83 for b in range(300)], [9000] + [3] * 40 + [-1] * 5 + [700]):
+        cache, q, cl, _ = batch(p, cached, [1] * len(cached), 64, BF)
+        out, lse, ws = run_decode(p, cache, q, cl)
+        assert ok(ws) == 0
+        check_batch(p, cache, cached, [1] * len(cached), q, out, lse, BF)
+        again, lse2, _ = run_decode(p, cache, q, cl, ws)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)      # sums in one order
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_decode_large_scores(dt):
+    """Scores of some hundreds: the running maximum rises along the way."""
+    p = qsa.layer_params(24, 2, 256, dtype=dt, softmax_scale=1.0)
+    cached = [2000, 77]
+    cache, q, cl, _ = batch(p, cached, [1, 1], 16, dt, spread=4.0)
+    out, lse, ws = run_decode(p, cache, q, cl)
+    assert ok(ws) == 0
+    check_batch(p, cache, cached, [1, 1], q, out, lse, dt)
+
+
+def test_decode_bad_pages_are_masked_and_reported():
+    p = qsa.layer_params(24, 2, 256)
+    cached = [100, 100, 30, 5]
+    cache, q, cl, _ = batch(p, cached, [1] * 4, 16, BF)
+    bad = cache.table.clone()
+    cache.table[0, 2] = 1 << 30                                        # keys 32 .. 47 of sequence 0
+    cache.table[2] = -1                                                # all of sequence 2
+    out, lse, ws = run_decode(p, cache, q, cl)
+    assert ok(ws) == 7 and ok(ws) == 0
+    cache.table.copy_(bad)
+    keys = torch.cat([torch.arange(32), torch.arange(48, 101)]).cuda()
+    U.check_row(out[0], lse[0], U.attend64(p, q[0], *cache.rows(0, keys)), BF)
+    assert bool((out[2] == 0).all()) and bool((lse[2] == -float("inf")).all())
+    for b in (1, 3):
+        U.check_row(out[b], lse[b], U.attend64(p, q[b], *cache.rows(b, U.visible(p, cached[b]).cuda())), BF)
+    # a length past the table: what the table holds
+    cl2 = torch.tensor([100, 10 ** 6, -1, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    out, lse, ws = run_decode(p, cache, q, cl2)
+    assert ok(ws) == 7
+    U.check_row(out[0], lse[0], U.attend64(p, q[0], *cache.rows(0, U.visible(p, 100).cuda())), BF)
+
+
+def test_decode_captured_follows_lengths():
+    """A graph of append and decode replayed at growing lengths, a sequence leaving on the way."""
+    hq, hk, D, B, page = 24, 2, 256, 5, 16
+    p = qsa.layer_params(hq, hk, D)
+    cache = U.Cache(p, [400] * B, page, BF, "cuda")
+    g = gen(2)
+    start = [0, 15, 16, 200, 333]
+    for b, n in enumerate(start):
+        cache.fill(b, 0, n, randn(g, BF, n, hk, D), randn(g, BF, n, hk, D))
+    cl = torch.tensor(start, dtype=torch.int32, device="cuda")
+    q, k, v = randn(g, BF, B, hq, D), randn(g, BF, B, hk, D), randn(g, BF, B, hk, D)
+    qo, out = torch.zeros_like(q), torch.zeros_like(q)
+    lse = torch.zeros(B, hq, device="cuda")
+    ws = qsa.paged_workspace(p, B, B)
+
+    def step(s):
+        qsa.qsa_paged_append(p, cache.kv, B, B, None, cl, k, v, ws, q=q, q_out=qo, stream=s)
+        qsa.qsa_paged_decode(p, cache.kv, B, cl, qo, out, ws, lse=lse, stream=s)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    keep = cl.clone()
+    cl.fill_(-1)                                                       # warm up on nothing
+    with torch.cuda.stream(side):
+        step(side)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(torch.cuda.current_stream())
+    cl.copy_(keep)
+    for i in range(20):
+        for t in (q, k, v):
+            t.copy_(randn(g, BF, *t.shape))
+        graph.replay()
+        lens = cl.tolist()
+        check_batch(p, cache, lens, [1] * B, qo, out, lse, BF)
+        cl += (cl >= 0).int()
+        if i == 9:
+            cl[3] = -1
+    assert ok(ws) == 0
+
+
+def test_offsets_past_32_bits():
+    """Pages and rows more than 2^31 elements into the pool."""
+    hq, hk, D, page = 24, 2, 256, 64
+    p = qsa.layer_params(hq, hk, D)
+    n_pages = (1 << 31) // (page * hk * D) + 9                         # 4.3 GB of keys, as much of values
+    k = torch.empty(n_pages, page, hk, D, dtype=BF, device="cuda")
+    v = torch.empty_like(k)
+    ids = [n_pages - 1, 0, n_pages - 2]
+    table = torch.tensor([ids], dtype=torch.int32, device="cuda")
+    g = gen(4)
+    n = 3 * page
+    kn, vn, q = randn(g, BF, n, hk, D), randn(g, BF, n, hk, D), randn(g, BF, n, hq, D)
+    kv = qsa.PagedKV(k, v, table)
+    ws = qsa.paged_workspace(p, 1, n)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    cl = torch.zeros(1, dtype=torch.int32, device="cuda")
+    plain = qsa.layer_params(hq, hk, D, rope_dim=0)
+    qsa.qsa_paged_append(plain, kv, 1, n, cu, cl, kn, vn, ws)
+    assert torch.equal(k[ids].flatten(0, 1), kn) and torch.equal(v[ids].flatten(0, 1), vn)
+    out, lse = torch.zeros_like(q), torch.zeros(n, hq, device="cuda")
+    qsa.qsa_paged_prefill(p, kv, 1, n, cu, cl, q, out, ws, lse=lse)
+    for i in (0, 63, 64, 130, n - 1):
+        U.check_row(out[i], lse[i], U.attend64(p, q[i], kn[:i + 1].double(), vn[:i + 1].double()), BF)
+    o1, l1 = torch.zeros(1, hq, D, dtype=BF, device="cuda"), torch.zeros(1, hq, device="cuda")
+    qsa.qsa_paged_decode(p, kv, 1, torch.tensor([n - 1], dtype=torch.int32, device="cuda"), q[n - 1:], o1, ws, lse=l1)
+    U.check_row(o1[0], l1[0], U.attend64(p, q[n - 1], kn.double(), vn.double()), BF)
+    assert ok(ws) == 0
+
+
+def run_prefill(p, cache, q, cl, cu, ws=None):
+    B, T = cl.shape[0], q.shape[0]
+    out = torch.full_like(q, 9.0)
+    lse = torch.full(q.shape[:2], 9.0, dtype=torch.float32, device="cuda")
+    ws = qsa.paged_workspace(p, B, T) if ws is None else ws
+    qsa.qsa_paged_prefill(p, cache.kv, B, T, cu, cl, q, out, ws, lse=lse)
+    return out, lse, ws
+
+
+def some(n):
+    return {0, 1, 9, 10, 11, n // 3, n // 2, n - 2, n - 1}
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("dt,page,layout", [(BF, 16, "token"), (FP, 48, "head"), (BF, 1, "beside"), (FP, 128, "token")])
+def test_prefill(heads, dt, page, layout):
+    p = qsa.layer_params(*heads, dtype=dt)
+    cached, new = [0, 3, 130, -1, 0, 1000, 127], [1, 200, 5, 7, 0, 40, 131]
+    cache, q, cl, cu = batch(p, cached, new, page, dt, layout)
+    out, lse, ws = run_prefill(p, cache, q, cl, cu)
+    assert ok(ws) == 0
+    check_batch(p, cache, cached, new, q, out, lse, dt, some)
+    pad = slice(int(cu[3]), int(cu[4]))
+    assert bool((out[pad] == 9).all()) and bool((lse[pad] == 9).all())
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (100, 0), (100, 64), (100, 300), (1000, 4)])
+@pytest.mark.parametrize("heads", [(24, 2, 256), (28, 4, 128), (16, 16, 64)])
+def test_prefill_window(heads, window, sinks):
+    p = qsa.layer_params(*heads, window=window, n_sinks=sinks)
+    cached, new = [0, 2 * window + 77, window, 0], [300, 130, 1, 2 * window + 9 if window < 500 else 3]
+    g = gen(window)
+    cache, q, cl, cu = batch(p, cached, new, 16, BF, seed=window)
+    # a token in the middle of a chunk may see more than the ends: every page from the first window on is there
+    out, lse, ws = run_prefill(p, cache, q, cl, cu)
+    assert ok(ws) == 0
+    check_batch(p, cache, cached, new, q, out, lse, BF, some)
+    assert g is not None
+
+
+def test_prefill_long_prefix_few_rows():
+    """A short chunk over a long prefix."""
+    p = qsa.layer_params(24, 2, 256)
+    for cached, new in (([20011], [5]), ([9000, 12, 7001], [37, 3, 1])):
+        cache, q, cl, cu = batch(p, cached, new, 64, BF)
+        out, lse, ws = run_prefill(p, cache, q, cl, cu)
+        assert ok(ws) == 0
+        check_batch(p, cache, cached, new, q, out, lse, BF)
+        again, lse2, _ = run_prefill(p, cache, q, cl, cu, ws)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_prefill_large_scores(dt):
+    p = qsa.layer_params(24, 2, 256, dtype=dt, softmax_scale=1.0)
+    cached, new = [700, 0], [60, 300]
+    cache, q, cl, cu = batch(p, cached, new, 16, dt, spread=4.0)
+    out, lse, ws = run_prefill(p, cache, q, cl, cu)
+    assert ok(ws) == 0
+    check_batch(p, cache, cached, new, q, out, lse, dt, some)
+
+
+def test_prefill_bad_pages_and_rows_behind():
+    p = qsa.layer_params(24, 2, 256)
+    cached, new = [50, 0, 30], [20, 40, 10]
+    cache, q, cl, cu = batch(p, cached, new, 16, BF)
+    good = cache.table.clone()
+    cache.table[0, 1] = 1 << 29                                        # keys 16 .. 31 of sequence 0
+    cache.table[2] = -3
+    q2 = torch.cat([q, q[:6]])                                         # six rows behind the last sequence
+    out, lse, ws = run_prefill(p, cache, q2, cl, cu)
+    assert ok(ws) == 7 and ok(ws) == 0
+    cache.table.copy_(good)
+    for i in range(20):
+        keys = torch.cat([torch.arange(16), torch.arange(32, 51 + i)]).cuda()
+        U.check_row(out[i], lse[i], U.attend64(p, q[i], *cache.rows(0, keys)), BF)
+    check_batch(p, cache, [-1, 0, -1], new, q, out, lse, BF)
+    assert bool((out[60:70] == 0).all()) and bool((lse[60:70] == -float("inf")).all())
+    assert bool((out[70:] == 9).all()) and bool((lse[70:] == 9).all())
+
+
+def test_prefill_of_one_token_each_is_a_decode():
+    p = qsa.layer_params(24, 2, 256, window=64, n_sinks=4)
+    cached = [0, 5, 63, 64, 200, 1000]
+    cache, q, cl, cu = batch(p, cached, [1] * 6, 16, BF)
+    a, la, _ = run_decode(p, cache, q, cl)
+    b, lb, _ = run_prefill(p, cache, q, cl, cu)
+    assert float((a.double() - b.double()).abs().max()) < 2e-2 and float((la - lb).abs().max()) < 1e-4
+
+
+# ---------------------------------------------------------------- a run of them
+def test_dense_layer_equals_qsa_prefill():
+    """While the budget covers every block, QSA is dense causal attention: the
+    paged calls give what qsa_prefill gives on the same tokens."""
+    T = 1000
+    g = gen(8)
+    q, k, v = randn(g, BF, T, 24, 256), randn(g, BF, T, 2, 256), randn(g, BF, T, 2, 256)
+    w = torch.softmax(torch.randn(T, 4, generator=g), -1).to(BF).cuda()
+    r = qsa.prefill(q, k, v, randn(g, BF, T, 4, 128), w, randn(g, BF, T, 128), budget=512)
+    p = qsa.layer_params()
+    cache = U.Cache(p, [T], 64, BF, "cuda")
+    ws = qsa.paged_workspace(p, 1, T)
+    cu, cl = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, T], [0]))
+    qo, out, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(T, 24, device="cuda")
+    qsa.qsa_paged_append(p, cache.kv, 1, T, cu, cl, k, v, ws, q=q, q_out=qo)
+    qsa.qsa_paged_prefill(p, cache.kv, 1, T, cu, cl, qo, out, ws, lse=lse)
+    assert ok(ws) == 0 and qsa.qsa_check_device_error(r["ws"]) == 0
+    want = r["out"].view(BF).double()
+    diff = out.double() - want
+    assert float(diff.abs().max()) < 2e-2 and float(diff.norm() / want.norm()) < 5e-3
+    assert float((lse - r["lse"]).abs().max()) < 2e-2
+
+
+def test_norms_feed_qsa_prefill():
+    """With rope_dim 0 the normed queries and keys go into qsa_prefill, which rotates them."""
+    T = 500
+    g = gen(10)
+    qkv = randn(g, BF, T, 28, 256)
+    qw, kw = 0.1 * randn(g, BF, 256), 0.1 * randn(g, BF, 256)
+    qn, kn = torch.empty(T, 24, 256, dtype=BF, device="cuda"), torch.empty(T, 2, 256, dtype=BF, device="cuda")
+    qsa.qsa_norm_rope(qsa.layer_params(rope_dim=0), T, 0, qkv[:, :24], qkv[:, 24:26], qw, kw, qn, kn)
+    w = torch.softmax(torch.randn(T, 4, generator=g), -1).to(BF).cuda()
+    r = qsa.prefill(qn, kn, qkv[:, 26:].contiguous(), randn(g, BF, T, 4, 128), w, randn(g, BF, T, 128), budget=512)
+    p = qsa.layer_params()
+    pos = torch.arange(T, device="cuda")[None]
+    qr, _ = U.norm_rope64(p, qkv[:, :24], qw, pos)
+    kr, _ = U.norm_rope64(p, qkv[:, 24:26], kw, pos)
+    torch.cuda.synchronize()
+    for i in (0, 1, 7, 250, 499):
+        want, *_ = U.attend64(p, qr[i], kr[:i + 1], qkv[:i + 1, 26:].double())
+        assert float((r["out"][i].view(BF).double() - want).abs().max()) < 3e-2
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (48, 4)])
+def test_serving_run(window, sinks):
+    """Prompts in chunks, then decode steps, norms and three-axis positions on the
+    way, against attention over everything in 64 bits."""
+    hq, hk, D, page = 12, 2, 128, 16
+    p = qsa.layer_params(hq, hk, D, rope_dim=64, rope_axes=3, window=window, n_sinks=sinks)
+    prompt, steps = [70, 5, 133], 6
+    B = len(prompt)
+    total = [n + steps for n in prompt]
+    cache = U.Cache(p, total, page, BF, "cuda")
+    g = gen(12)
+    qkv = [randn(g, BF, n, hq + 2 * hk, D) for n in total]
+    qw, kw = 0.2 * randn(g, BF, D), 0.2 * randn(g, BF, D)
+    pos = [torch.stack([torch.arange(n), torch.arange(n) // 3, torch.arange(n) % 7]).int().cuda() for n in total]
+    ws = qsa.paged_workspace(p, B, sum(total))
+    got = [torch.empty(n, hq, D, dtype=BF, device="cuda") for n in total]
+    done = [0] * B
+
+    def step(new):
+        x = torch.cat([qkv[b][done[b]:done[b] + n] for b, n in enumerate(new)])
+        ps = torch.cat([pos[b][:, done[b]:done[b] + n] for b, n in enumerate(new)], 1).contiguous()
+        T = x.shape[0]
+        cu = torch.tensor([0] + list(torch.tensor(new).cumsum(0)), dtype=torch.int32, device="cuda")
+        cl = torch.tensor(done, dtype=torch.int32, device="cuda")
+        qo = torch.empty(T, hq, D, dtype=BF, device="cuda")
+        out = torch.empty_like(qo)
+        qsa.qsa_paged_append(p, cache.kv, B, T, cu, cl, x[:, hq:hq + hk], x[:, hq + hk:], ws, q=x[:, :hq], q_out=qo,
+                             q_weight=qw, k_weight=kw, positions=ps)
+        if max(new) == 1:
+            qsa.qsa_paged_decode(p, cache.kv, B, cl, qo, out, ws)
+        else:
+            qsa.qsa_paged_prefill(p, cache.kv, B, T, cu, cl, qo, out, ws)
+        row = 0
+        for b, n in enumerate(new):
+            got[b][done[b]:done[b] + n] = out[row:row + n]
+            done[b] += n
+            row += n
+
+    step([50, 5, 64])
+    step([20, 0, 69])
+    for _ in range(steps):
+        step([1] * B)
+    assert ok(ws) == 0
+    for b in range(B):
+        x = qkv[b]
+        # the rounded queries and keys that the calls hand on
+        qr = U.norm_rope64(p, x[:, :hq], qw, pos[b])[0].to(BF)
+        kr = U.norm_rope64(p, x[:, hq:hq + hk], kw, pos[b])[0].to(BF).double()
+        for i in {0, 4, 49, 50, total[b] - steps - 1, total[b] - steps, total[b] - 1}:
+            if i < total[b]:
+                keys = U.visible(p, i).cuda()
+                want, *_ = U.attend64(p, qr[i], kr[keys], x[keys][:, hq + hk:].double())
+                assert float((got[b][i].double() - want).abs().max()) < 3e-2, (b, i)
