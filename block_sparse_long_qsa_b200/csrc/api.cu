@@ -1105,9 +1105,6 @@ qsa_status check_layer(const qsa_layer_params* p) {
       for (int a = 0; a < 3; ++a)
         if (n[a] < 0 || n[a] > half) return QSA_ERR_INVALID_ARG;
       if (n[0] + n[1] + n[2] != half) return QSA_ERR_INVALID_ARG;
-      // interleaved: the last pair of height (3 n - 2) and of width (3 n - 1) exists
-      if (p->rope_interleaved && ((n[1] > 0 && 3 * n[1] - 2 >= half) || (n[2] > 0 && 3 * n[2] - 1 >= half)))
-        return QSA_ERR_INVALID_ARG;
     }
   }
   if (!(p->norm_eps > 0.f) || !std::isfinite(p->norm_eps)) return QSA_ERR_INVALID_ARG;

@@ -404,7 +404,8 @@ typedef struct {
   /* rope_axes 1: one position per token.  3: positions of time, height and
    * width; rope_section[a] of the rope_dim/2 pairs turn by axis a (their sum
    * is rope_dim/2).  rope_interleaved 1: pair i turns by axis i % 3 while i <
-   * 3 * rope_section[i % 3] (height and width), all other pairs by time.  0:
+   * 3 * rope_section[i % 3] (height and width), all other pairs by time (where
+   * a section runs past the last pair, it has fewer and time the more).  0:
    * the first rope_section[0] pairs turn by time, the next by height, the
    * rest by width. */
   int32_t rope_axes;
