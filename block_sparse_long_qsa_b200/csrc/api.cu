@@ -1344,9 +1344,14 @@ qsa_status qsa_paged_prefill(const qsa_layer_params* p, const qsa_paged_kv* kv, 
   a.err = static_cast<uint32_t*>(ws);
   a.scratch = static_cast<uint8_t*>(ws) + HEADER_BYTES;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return from_cuda(traced(QSA_KERNEL_PAGED_PREFILL, s, [&] {
-    return qsa::launch_paged_prefill(a, p->head_dim, p->dtype, di.num_sms, s, false);
-  }), "paged prefill launch");
+  if ((st = from_cuda(traced(QSA_KERNEL_PAGED_PREFILL, s, [&] {
+         return qsa::launch_paged_prefill(a, p->head_dim, p->dtype, di.num_sms, s, false);
+       }), "paged prefill launch")) != QSA_OK)
+    return st;
+  if (!qsa::paged_prefill_splits(a, di.num_sms)) return QSA_OK;
+  return from_cuda(traced(QSA_KERNEL_PAGED_PREFILL_JOIN, s, [&] {
+    return qsa::launch_paged_prefill(a, p->head_dim, p->dtype, di.num_sms, s, true);
+  }), "paged prefill join launch");
 }
 
 }  // extern "C"

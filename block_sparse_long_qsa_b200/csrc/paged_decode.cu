@@ -96,7 +96,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_decode_kernel(const __grid_c
     for (int b0 = 0; b0 < a.B; b0 += THREADS) {
       const int b = b0 + tid;
       int u = 0;
-      if (b < a.B) u = (Visible(a, a.cache_len[b], a.err).n + UNIT - 1) / UNIT;
+      if (b < a.B) {
+        const int L = a.cache_len[b];
+        // at least one unit: a row whose keys all lie past the table comes out zero
+        if (L >= 0) u = max((Visible(a, L, a.err).n + UNIT - 1) / UNIT, 1);
+      }
       int s = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {

@@ -1,226 +1,639 @@
-// Attention of a ragged batch of new tokens over their pages (qsa_paged_prefill).
+// Attention of a ragged batch of new tokens over their pages (qsa_paged_prefill)
+// on the 5th-generation tensor cores.
 //
-// Item = (64 query rows of one sequence, KV head); the rows are the sequence's
-// (token, query head of the KV head) pairs laid out flat, so every head count
-// fills the tiles.  One pass over the visible keys with a running maximum and sum.
+//   out[t][h] = sum_j softmax_j(q[t][h] . k[j] scale) v[j]
+//
+// over the keys j up to the token's own that window and sinks leave; one pass
+// with a running maximum and sum.
+//
+// Item = (128 query rows of one sequence, KV head, range of keys); the rows are
+// the sequence's (token, query head of the KV head) pairs laid out flat, so any
+// head count fills the tiles and the heads of a KV head share its loads.  The
+// keys that any row sees are numbered without the gap between sinks and window
+// and taken in tiles of 128.  Persistent CTAs (one per SM) walk the items, those
+// of the last tokens (the most keys) first.
+//   * warps 0-7 (softmax): two threads a query row (TMEM lane), each with half
+//     of a tile's 128 scores: mask, running maximum in base 2 (the halves swap
+//     their tile maxima; it is raised only when a tile exceeds it by more than
+//     8, so the rescale of O is rare), exp2, P packed to 16 bits into the score
+//     buffer; at the end O / l and the log-sum-exp.
+//   * warps 8-11 (loaders): the Q tile, then K and V by cp.async, 16 bytes a
+//     thread, rows found through the page table, rows that no query sees zero.
+//     Slots of 16 KB in one ring: K as 128 keys x 64 dims, V as 128 * 64 / D
+//     keys x D dims, in the order the products take them.
+//   * warp 12 (one thread): S(i + 1) = Q K^T (M = 128, N = 128) is issued before
+//     O += P V (N = D) of tile i, so the tensor cores work on one while the
+//     softmax makes the other's operand.
+// Every mbarrier wait is bounded (timeout -> error word, clean exit): on an abort
+// every role leaves its loop, the loaders wait for their own copies and the MMA
+// thread for its last commit before TMEM is released.
+//
+// With few rows (a short chunk over a long prefix) an item's keys are cut into
+// n_split ranges so that the SMs fill up; the ranges' results go to the scratch
+// as normalised fp32 rows with their log-sum-exp, and the join kernel adds them
+// in the order of the keys.
 #include <cfloat>
+#include <type_traits>
 
 #include "paged.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int WARPS = 4;
-constexpr int THREADS = 32 * WARPS;
-constexpr int ROWS = 16 * WARPS;
-constexpr int KT = 32;
+constexpr int KT = 128;                             // keys of a tile
+constexpr int M = 128;                              // query rows of an item
+constexpr int LWARPS = 4;                           // loader warps (more leave the softmax fewer than 128 registers)
+constexpr int W_LOAD = 8, W_MMA = W_LOAD + LWARPS;
+constexpr int LOADERS = 32 * LWARPS;
+constexpr int THREADS = 32 * (W_MMA + 1);
+constexpr int RT = LOADERS / 8, RJ = KT / RT;       // rows of a loader pass, passes of a tile
+constexpr uint32_t SLOT = 16384;
+constexpr int NS = 10;                              // slots of the ring
+constexpr uint32_t OFF_RING = 65536;                // Q: up to 128 rows x 512 B
+constexpr uint32_t OFF_XCH = OFF_RING + NS * SLOT;  // softmax exchange [2][2][128] floats
+constexpr uint32_t OFF_OK = OFF_XCH + 2048;         // rows that are there, of NOK tiles, 32 bytes each
+// tiles whose row bits are live: the loaders run at most 6 tiles ahead of S (D =
+// 64: the ring holds 5), S 2 ahead of the softmax
+constexpr int NOK = 16;
+constexpr uint32_t OFF_BAR = OFF_OK + 32 * NOK;
+constexpr uint32_t SMEM = OFF_BAR + 320;
+static_assert(SMEM <= 232448, "prefill smem");
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TM_S = 0, TM_O = 256;            // S / P buffers at 0 and 128
+constexpr int MAX_PIECES = 160;                     // bound of the scratch
+constexpr int MAX_SPLIT = 32;
+constexpr float RAISE = 8.f;                        // lazy maximum: P stays below 2^8
 
-template <int D>
-constexpr uint32_t smem_bytes() {
-  return (ROWS + 4 * KT) * D * 2 + 64;
+__device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t c16) {
+  return row * 128u + ((c16 ^ (row & 7u)) << 4);
+}
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// MN-major operand descriptor (128-byte swizzle): lbo = distance between
+// 64-element atoms along N, sbo = distance between 8-row groups along K.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
+         (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+// O[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+struct Grid {
+  int64_t n_slots;          // tile slots of the batch
+  int n_split;
+};
+struct Scratch {
+  float* lse2;              // [MAX_PIECES][128]
+  float* o;                 // [MAX_PIECES][128][D]
+};
+__host__ __device__ inline Scratch scratch_of(void* p) {
+  return {static_cast<float*>(p), static_cast<float*>(p) + MAX_PIECES * M};
 }
 
+struct Args {
+  PagedAttnArgs a;
+  Grid grid;
+};
+
+// Item w.  Sequence b owns the tile slots from cu[b] per / 128 + b on (at least
+// as many as it has tiles), so a slot's sequence is found by bisection and the
+// slots without a tile are items without keys.
+struct Item {
+  int b, g, rows;           // sequence, KV head, rows in use
+  int n_tiles, tile0;       // tiles of this range, its first
+  int pieces, split;        // ranges that the item's keys are cut into, which one this is
+  int lo, ns, n_vis;        // visible key v: v < ns ? v : lo + v - ns
+  int p0;                   // position of the first row's token
+  int64_t t0, row0;         // the sequence's first token row; first flat row of the item
+  __device__ __forceinline__ Item(const Args& x, int64_t w) {
+    const PagedAttnArgs& a = x.a;
+    const int per = a.hq / a.hk, ns_ = x.grid.n_split;
+    n_tiles = 0;
+    tile0 = 0;
+    split = (int)(w % ns_);
+    w /= ns_;
+    g = (int)(w % a.hk);
+    const int64_t slot = x.grid.n_slots - 1 - w / a.hk;
+    int l = 0, h = a.B;
+    while (h - l > 1) {
+      const int mid = (l + h) >> 1;
+      if ((int64_t)__ldg(a.cu_new + mid) * per / M + mid <= slot) l = mid; else h = mid;
+    }
+    b = l;
+    t0 = __ldg(a.cu_new + b);
+    const int64_t t1 = min((int64_t)__ldg(a.cu_new + b + 1), a.T);
+    const int L = __ldg(a.cache_len + b);
+    const int64_t tile = slot - (t0 * per / M + b), n_rows = (t1 - t0) * per;
+    row0 = tile * M;
+    rows = (int)min((int64_t)M, n_rows - row0);
+    if (t0 < 0 || tile < 0 || rows <= 0 || L < 0) return;
+    const int64_t first = L + row0 / per, last = L + (row0 + rows - 1) / per;
+    const int end = (int)min(last + 1, (int64_t)a.kv.capacity);
+    if (last >= a.kv.capacity) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
+    lo = a.window > 0 && first >= a.window ? (int)min(first - a.window + 1, (int64_t)end) : 0;
+    ns = min(a.sinks, lo);
+    n_vis = ns + end - lo;
+    p0 = (int)min(first, (int64_t)INT32_MAX);
+    // at least one tile: rows whose keys all lie past the table come out zero
+    const int all = max((n_vis + KT - 1) / KT, 1), each = (all + ns_ - 1) / ns_;
+    pieces = (all + each - 1) / each;
+    tile0 = split * each;
+    n_tiles = min(each, all - tile0);
+  }
+};
+
 template <class E, int D>
-__global__ void __launch_bounds__(THREADS) paged_prefill_kernel(const __grid_constant__ PagedAttnArgs a) {
-  constexpr int G = D / 8, NK = KT / 8, NO = D / 8;
+__global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_constant__ Args x) {
+  constexpr int NCH = D / 64;                       // 64-dim chunks: K (and V) slots of a tile
+  constexpr int KV = KT / NCH;                      // keys of a V slot
+  constexpr uint32_t IDESC = umma_idesc_bf16_f32(M, KT) &
+                             (std::is_same<E, __half>::value ? ~((1u << 7) | (1u << 10)) : ~0u);   // f16: 0
+  constexpr uint32_t IDESC_PV = ((IDESC & ~(63u << 17)) | ((uint32_t)(D >> 3) << 17)) | (1u << 16);   // V MN-major
   using X = Elem<E>;
+  const PagedAttnArgs& a = x.a;
   extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* full = bars;                            // [NS]
+  uint64_t* empty = full + NS;                      // [NS]
+  uint64_t* q_full = empty + NS;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;                   // [2]
+  uint64_t* p_full = s_full + 2;                    // [2]
+  uint64_t* pv_done = p_full + 2;                   // [2]
+  uint64_t* o_empty = pv_done + 2;
+  uint64_t* xbar = o_empty + 1;                     // [4]: 32 rows each
+  uint64_t* mma_done = xbar + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint64_t* rows_ok = reinterpret_cast<volatile uint64_t*>(smem + OFF_OK);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t q_base = smem_u32(smem), kv_base = q_base + ROWS * D * 2;
-  uint32_t* vmask = reinterpret_cast<uint32_t*>(smem + (ROWS + 4 * KT) * D * 2);   // [2]
-  const int per = a.hq / a.hk, g = blockIdx.y;
-  // Tile slots: sequence b owns the slots from cu[b] per / 64 + b on (at least as
-  // many as it has tiles).  The last slots come first.
-  const int64_t slot = (int64_t)gridDim.x - 1 - blockIdx.x;
-  int b = 0;
-  {
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((int64_t)a.cu_new[mid] * per / ROWS + mid <= slot) lo = mid; else hi = mid;
-    }
-    b = lo;
+  if ((smem_u32(smem) & 1023u) != 0u) {
+    if (tid == 0) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
+    return;
   }
-  const int64_t t0 = a.cu_new[b], t1 = min((int64_t)a.cu_new[b + 1], a.T);
-  const int64_t tile = slot - (t0 * per / ROWS + b);
-  const int64_t n_rows = (t1 - t0) * per;
-  const int L = a.cache_len[b];
-  if (t0 < 0 || tile < 0 || tile * ROWS >= n_rows || L < 0) return;
-  const int64_t row0 = tile * ROWS;
-  const int rows = (int)min((int64_t)ROWS, n_rows - row0);
-  // positions of the first and the last row's tokens
-  const int64_t p_first = L + row0 / per, p_last = L + (row0 + rows - 1) / per;
-  if (p_last >= a.kv.capacity && tid == 0) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
-  const int end = (int)min(p_last + 1, (int64_t)a.kv.capacity);
-  int lo = a.window > 0 && p_first >= a.window ? (int)(p_first - a.window + 1) : 0;
-  if (lo > end) lo = end;
-  const int ns = min(a.sinks, lo), n_vis = ns + end - lo;
-  const int n_tiles = (n_vis + KT - 1) / KT;
-  const int32_t* table = a.kv.table + (int64_t)b * a.kv.table_ld;
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) { mbar_init(&full[s], LOADERS); mbar_init(&empty[s], 1); }
+    mbar_init(q_full, LOADERS);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8); mbar_init(&pv_done[i], 1); }
+    mbar_init(o_empty, 8);
+    for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 64);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == W_MMA) { tmem_alloc(tmem_slot, TMEM_COLS); tmem_relinquish(); }
+  pdl_launch();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t n_items = x.grid.n_slots * a.hk * x.grid.n_split;
+  const int per = a.hq / a.hk;
 
-  // queries
-  for (int e = tid; e < ROWS * G; e += THREADS) {
-    const int r = e / G, c = e % G;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const int64_t f = row0 + r;
-      v = __ldg(reinterpret_cast<const uint4*>(a.q + ((t0 + f / per) * a.hq + g * per + f % per) * D) + c);
+  if (warp >= W_LOAD && warp < W_MMA) {
+    // ---------------------------------------------------------------- loaders
+    const int lt = tid - 32 * W_LOAD, c = lt & 7, rt = lt >> 3;   // 16-byte chunk, row of a pass
+    int slot = 0;
+    uint32_t eph = 1, items_done = 0, count = 0;   // tiles so far
+    bool ok = true;
+    auto advance = [&]() { if (++slot == NS) { slot = 0; eph ^= 1; } };
+    for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
+      const Item it(x, w);
+      if (it.n_tiles <= 0) continue;
+      const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
+      const int64_t head = (int64_t)it.g * a.kv.head_stride + 8 * c;
+      // this thread's rows rt + RT j of a tile, for K and V alike: offset of its
+      // chunk of the row, or -1
+      int64_t off_k[RJ], off_v[RJ];
+      auto find_rows = [&](int tile) {
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) {
+          const int v = tile * KT + RT * j + rt;
+          off_k[j] = -1;
+          if (v < it.n_vis) {
+            const int64_t o = page_row(a.kv, table, v < it.ns ? v : it.lo + (v - it.ns), a.err);
+            if (o >= 0) off_k[j] = o + head;
+          }
+          // the warp's four rows of the pass: one byte of their bits
+          const uint32_t bits = __ballot_sync(0xffffffffu, off_k[j] >= 0 && c == 0);
+          if (lane == 0) {
+            const uint32_t four = (bits & 1) | (bits >> 7 & 2) | (bits >> 14 & 4) | (bits >> 21 & 8);
+            reinterpret_cast<volatile uint8_t*>(rows_ok)[(count % NOK) * 32 + j * LWARPS + (warp - W_LOAD)] = (uint8_t)four;
+          }
+        }
+      };
+      auto load_k = [&]() -> bool {
+#pragma unroll
+        for (int ch = 0; ch < NCH; ++ch) {
+          if (!mbar_wait(&empty[slot], eph, abort_flag, a.err)) return false;
+          const uint32_t dst = smem_u32(smem + OFF_RING + slot * SLOT);
+#pragma unroll
+          for (int j = 0; j < RJ; ++j) {
+            const bool valid = off_k[j] >= 0;
+            cp_async16_zfill(dst + swz128(RT * j + rt, c), valid ? a.kv.k + off_k[j] + 64 * ch : a.kv.k, valid);
+          }
+          cp_async_arrive(&full[slot]);
+          advance();
+        }
+        return true;
+      };
+      auto load_v = [&]() -> bool {
+#pragma unroll
+        for (int s = 0; s < NCH; ++s) {
+          if (!mbar_wait(&empty[slot], eph, abort_flag, a.err)) return false;
+          const uint32_t dst = smem_u32(smem + OFF_RING + slot * SLOT);
+#pragma unroll
+          for (int j = 0; j < KV / RT; ++j) {
+            const int64_t o = off_v[s * (KV / RT) + j];
+            const bool valid = o >= 0;
+#pragma unroll
+            for (int ch = 0; ch < NCH; ++ch)
+              cp_async16_zfill(dst + ch * (KV * 128) + swz128(RT * j + rt, c), valid ? a.kv.v + o + 64 * ch : a.kv.v,
+                               valid);
+          }
+          cp_async_arrive(&full[slot]);
+          advance();
+        }
+        return true;
+      };
+      for (int i = 0; ok && i <= it.n_tiles; ++i) {
+        if (i < it.n_tiles) {
+          find_rows(it.tile0 + i);
+          ++count;
+          if (!load_k()) { ok = false; break; }
+        }
+        if (i == 0) {
+          // queries, once the previous item's last S has read its own
+          if (items_done > 0 && !mbar_wait(q_empty, (items_done - 1) & 1, abort_flag, a.err)) { ok = false; break; }
+#pragma unroll
+          for (int j = 0; j < RJ; ++j) {
+            const int r = RT * j + rt;
+            const bool valid = r < it.rows;
+            const int64_t f = it.row0 + (valid ? r : 0);
+            const uint16_t* src = a.q + ((it.t0 + f / per) * a.hq + it.g * per + f % per) * D + 8 * c;
+#pragma unroll
+            for (int ch = 0; ch < NCH; ++ch)
+              cp_async16_zfill(smem_u32(smem + ch * SLOT) + swz128(r, c), valid ? src + 64 * ch : a.q, valid);
+          }
+          cp_async_arrive(q_full);
+        } else if (!load_v()) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) off_v[j] = off_k[j];
+      }
+      ++items_done;
     }
-    *reinterpret_cast<uint4*>(smem + row_chunk<D>(r, c)) = v;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == W_MMA) {
+    // -------------------------------------------------------------------- MMA
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t fph = 0, items_done = 0, s_count = 0, p_count = 0;
+      bool ok = true;
+      const uint32_t q_base = smem_u32(smem);
+      auto take = [&](uint32_t& base) -> bool {     // the next full slot
+        if (!mbar_wait(&full[slot], fph, abort_flag, a.err)) return false;
+        fence_async_proxy();                        // written by cp.async, read by the MMA
+        tc_fence_after();
+        base = smem_u32(smem + OFF_RING + slot * SLOT);
+        return true;
+      };
+      auto done = [&]() {
+        tc_commit(&empty[slot]);
+        if (++slot == NS) { slot = 0; fph ^= 1; }
+      };
+      for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
+        const Item it(x, w);
+        if (it.n_tiles <= 0) continue;
+        if (!mbar_wait(q_full, items_done & 1, abort_flag, a.err)) { ok = false; break; }
+        for (int i = 0; ok && i <= it.n_tiles; ++i) {
+          if (i < it.n_tiles) {
+            // S(i) overwrites the buffer of P(i - 2), which P V(i - 2), issued
+            // before it by this thread, has read by then
+            const uint32_t d = tmem + TM_S + 128 * (s_count & 1);
+            for (int ch = 0; ch < NCH; ++ch) {
+              uint32_t kb;
+              if (!take(kb)) { ok = false; break; }
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                umma_bf16(d, umma_desc_k_sw128(q_base + ch * SLOT + 32 * ks), umma_desc_k_sw128(kb + 32 * ks), IDESC,
+                          ch > 0 || ks > 0 ? 1u : 0u);
+              done();
+            }
+            if (!ok) break;
+            tc_commit(&s_full[s_count & 1]);
+            if (i == it.n_tiles - 1) tc_commit(q_empty);
+            ++s_count;
+          }
+          if (i > 0) {
+            const uint32_t p = tmem + TM_S + 128 * (p_count & 1);
+            if (!mbar_wait(&p_full[p_count & 1], (p_count >> 1) & 1, abort_flag, a.err)) { ok = false; break; }
+            if (i == 1 && items_done > 0 && !mbar_wait(o_empty, (items_done - 1) & 1, abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            for (int s = 0; s < NCH; ++s) {
+              uint32_t vb;
+              if (!take(vb)) { ok = false; break; }
+#pragma unroll
+              for (int ks = 0; ks < KV / 16; ++ks)
+                umma_ts(tmem + TM_O, p + 8 * (s * (KV / 16) + ks), desc_mn_sw128(vb + 2048 * ks, KV * 128, 1024),
+                        IDESC_PV, i > 1 || s > 0 || ks > 0 ? 1u : 0u);
+              done();
+            }
+            if (!ok) break;
+            tc_commit(&pv_done[p_count & 1]);
+            ++p_count;
+          }
+        }
+        ++items_done;
+      }
+      // every MMA this thread issued has retired before TMEM is released (also
+      // after an abort: a wait that ignores the flag)
+      tc_commit(mma_done);
+      mbar_wait_drain(mma_done, 0, a.err);
+    }
+  } else if (warp < W_LOAD) {
+    // ---------------------------------------------------------------- softmax
+    const int quad = warp & 3, half = warp >> 2;    // rows 32 quad .., scores 64 half ..
+    const int r = 32 * quad + lane;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    float* xch = reinterpret_cast<float*>(smem + OFF_XCH);   // [2][2 halves][128 rows]
+    uint32_t xc = 0, count = 0, items_done = 0;
+    bool ok = true;
+    auto exchange = [&](float mine, float& other) -> bool {
+      const uint32_t s = (xc & 1) * 2;
+      xch[(s + half) * M + r] = mine;
+      mbar_arrive(&xbar[quad]);
+      const bool okx = __all_sync(0xffffffffu, mbar_wait(&xbar[quad], xc & 1, abort_flag, a.err));
+      other = xch[(s + (half ^ 1)) * M + r];
+      ++xc;
+      return okx;
+    };
+    for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
+      const Item it(x, w);
+      if (it.n_tiles <= 0) continue;
+      const bool in = r < it.rows;
+      const int64_t flat = it.row0 + (in ? r : 0);
+      // the row sees v in [v_min, v_max] and v < sinks (in the numbering without the gap)
+      const int64_t pos = (int64_t)it.p0 + (flat / per - it.row0 / per);
+      const int v_max = (int)min(pos - it.lo + it.ns, (int64_t)it.n_vis - 1);
+      const int v_min = a.window > 0 ? (int)max(pos - a.window + 1 - it.lo + it.ns, (int64_t)0) : 0;
+      // the whole item's: every row sees v in [all_min, all_max]
+      const int64_t pos1 = (int64_t)it.p0 + ((it.row0 + it.rows - 1) / per - it.row0 / per);
+      const int all_max = (int)min((int64_t)it.p0 - it.lo + it.ns, (int64_t)it.n_vis - 1);
+      const int all_min = a.window > 0 ? (int)max(pos1 - a.window + 1 - it.lo + it.ns, (int64_t)0) : 0;
+      float m = -FLT_MAX, l = 0.f;
+      for (int i = 0; i < it.n_tiles; ++i, ++count) {
+        const uint32_t buf = count & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], (count >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t s_addr = tmem + lanes + TM_S + 128 * buf;
+        float s0[32], s1[32];
+        tmem_ld32(s_addr + 64 * half, s0);
+        tmem_ld32(s_addr + 64 * half + 32, s1);
+        tmem_ld_wait(s0);
+        tmem_ld_wait(s1);
+        const int v0 = (it.tile0 + i) * KT;
+        // the keys that are there, four to a byte
+        const uint64_t w0 = rows_ok[(count % NOK) * 4 + 2 * half], w1 = rows_ok[(count % NOK) * 4 + 2 * half + 1];
+        const bool whole = v0 + KT - 1 <= all_max && (v0 >= all_min || v0 + KT <= a.sinks) &&
+                           (w0 & w1) == 0x0f0f0f0f0f0f0f0full;
+        if (!whole) {
+          const int vb = v0 + 64 * half;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int va = vb + e, vc = va + 32;
+            const bool oka = va <= v_max && (va >= v_min || va < a.sinks) && (w0 >> ((e >> 2) * 8 + (e & 3)) & 1);
+            const bool okc = vc <= v_max && (vc >= v_min || vc < a.sinks) && (w1 >> ((e >> 2) * 8 + (e & 3)) & 1);
+            if (!oka) s0[e] = -INFINITY;
+            if (!okc) s1[e] = -INFINITY;
+          }
+        }
+        float mt = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) mt = max3f(mt, s0[e], s1[e]);
+        mt = fmaxf(mt * a.scale_log2, -FLT_MAX);    // a tile without a key leaves the maximum as it is
+        float other;
+        if (!exchange(mt, other)) { ok = false; break; }
+        mt = fmaxf(mt, other);
+        const bool raise = mt > m + RAISE;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float nm = raise ? mt : m;
+          const float f = exp2_approx(m - nm);
+          l *= f;
+          m = nm;
+          if (i > 0) {
+            // O holds the tiles up to i - 1 once their P V is done; this tile's
+            // waits for this warp
+            const uint32_t g = count - 1;
+            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[g & 1], (g >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < D / 64; ++cc) {
+              float o[32];
+              const uint32_t ad = tmem + lanes + TM_O + (D / 2) * half + 32 * cc;
+              tmem_ld32(ad, o);
+              tmem_ld_wait(o);
+              uint32_t u[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+              tmem_st32(ad, u);
+            }
+            tmem_st_wait();
+          }
+        }
+        // p = 2^(s scale - m); the sum takes the fp32 values, the products p rounded to 16 bits
+        uint32_t pk[32];
+        float l0 = 0.f, l1 = 0.f;
+        const float nm = -m;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float a0 = exp2_approx(fmaf(s0[2 * e], a.scale_log2, nm));
+          const float a1 = exp2_approx(fmaf(s0[2 * e + 1], a.scale_log2, nm));
+          const float b0 = exp2_approx(fmaf(s1[2 * e], a.scale_log2, nm));
+          const float b1 = exp2_approx(fmaf(s1[2 * e + 1], a.scale_log2, nm));
+          l0 += a0 + a1;
+          l1 += b0 + b1;
+          pk[e] = X::pack(a0, a1);
+          pk[16 + e] = X::pack(b0, b1);
+        }
+        l += l0 + l1;
+        tmem_st32(s_addr + 32 * half, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[buf]);
+      }
+      if (!ok) break;
+      // ---- O / l
+      const uint32_t g = count - 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[g & 1], (g >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
+      tc_fence_after();
+      float l_other;
+      if (!exchange(l, l_other)) { ok = false; break; }
+      const float lr = l + l_other;
+      const float inv = lr == 0.f ? 0.f : 1.f / lr;   // no key at all: zero
+      const float lse2 = lr == 0.f ? -INFINITY : m + log2f(lr);
+      const int64_t orow = (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
+      const bool part = it.pieces > 1;
+      const Scratch sc = scratch_of(a.scratch);
+      const int64_t prow = w * M + r;
+#pragma unroll 1
+      for (int cc = 0; cc < D / 64; ++cc) {
+        float o[32];
+        const int d0 = (D / 2) * half + 32 * cc;
+        tmem_ld32(tmem + lanes + TM_O + d0, o);
+        tmem_ld_wait(o);
+        if (in && part) {
+          float4* dst = reinterpret_cast<float4*>(sc.o + prow * D + d0);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv, o[4 * q + 3] * inv);
+        } else if (in) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + d0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            dst[q] = make_uint4(X::pack(o[8 * q] * inv, o[8 * q + 1] * inv), X::pack(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                                X::pack(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
+                                X::pack(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+        }
+      }
+      if (in && half == 0) {
+        if (part) sc.lse2[prow] = lse2;
+        else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_empty);
+      ++items_done;
+    }
   }
-  auto issue = [&](int i) {
-    if (i < n_tiles) {
-      const int v = i * KT + lane;
-      const int64_t off = v < n_vis ? page_row(a.kv, table, v < ns ? v : lo + (v - ns), a.err) : -1;
-      const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
-      if (tid == 0) vmask[i & 1] = ok;
-      const uint32_t kd = kv_base + (i & 1) * 2 * KT * D * 2, vd = kd + KT * D * 2;
-#pragma unroll
-      for (int j = 0; j < KT * G / THREADS; ++j) {
-        const int e = j * THREADS + tid, row = e / G, c = e % G;
-        const int64_t o = __shfl_sync(0xffffffffu, off, row) + g * a.kv.head_stride + 8 * c;
-        const bool valid = (ok >> row) & 1;
-        cp_async16_zfill(kd + row_chunk<D>(row, c), valid ? a.kv.k + o : a.kv.k, valid);
-        cp_async16_zfill(vd + row_chunk<D>(row, c), valid ? a.kv.v + o : a.kv.v, valid);
-      }
-    }
-    cp_async_commit();
-  };
-  issue(0);
-  float o[NO][4];
-#pragma unroll
-  for (int i = 0; i < NO; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  int64_t pos[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) pos[h] = L + (row0 + 16 * warp + (lane >> 2) + 8 * h) / per;
-  for (int i = 0; i < n_tiles; ++i) {
-    issue(i + 1);
-    cp_async_wait<1>();
-    __syncthreads();
-    const uint32_t ok = vmask[i & 1];
-    const uint32_t kd = kv_base + (i & 1) * 2 * KT * D * 2, vd = kd + KT * D * 2;
-    float s[NK][4];
-#pragma unroll
-    for (int n = 0; n < NK; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-    const uint32_t qr = 16 * warp + (lane & 7) + ((lane >> 3) & 1) * 8, kr = (lane >> 4) * 8 + (lane & 7);
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t qa[4];
-      ldsm4(qa, q_base + row_chunk<D>(qr, 2 * ks + (lane >> 4)));
-#pragma unroll
-      for (int n = 0; n < NK; n += 2) {
-        uint32_t kb[4];
-        ldsm4(kb, kd + row_chunk<D>(8 * n + kr, 2 * ks + ((lane >> 3) & 1)));
-        X::mma(s[n], qa, kb[0], kb[1]);
-        X::mma(s[n + 1], qa, kb[2], kb[3]);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NK; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = 8 * n + 2 * (lane & 3) + (e & 1), v = i * KT + c;
-        const int key = v < ns ? v : lo + (v - ns);
-        const int64_t ps = pos[e >> 1];
-        const bool seen = ((ok >> c) & 1) && key <= ps && (a.window == 0 || key > ps - a.window || key < a.sinks);
-        if (!seen) s[n][e] = -INFINITY;
-      }
-    float t[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int n = 0; n < NK; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[e >> 1] = fmaxf(t[e >> 1], s[n][e]);
-    float base[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      t[h] = fmaxf(t[h], __shfl_xor_sync(0xffffffffu, t[h], 1));
-      t[h] = fmaxf(t[h], __shfl_xor_sync(0xffffffffu, t[h], 2)) * a.scale_log2;
-      const float nm = fmaxf(m[h], t[h]);
-      const float f = nm == -INFINITY ? 1.f : exp2_approx(m[h] - nm);
-      m[h] = nm;
-      l[h] *= f;
-#pragma unroll
-      for (int n = 0; n < NO; ++n) {
-        o[n][2 * h] *= f;
-        o[n][2 * h + 1] *= f;
-      }
-      base[h] = nm == -INFINITY ? 0.f : nm;
-    }
-    uint32_t pa[KT / 16][4];
-#pragma unroll
-    for (int n = 0; n < NK; ++n) {
-      float p[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        p[e] = exp2_approx(fmaf(s[n][e], a.scale_log2, -base[e >> 1]));
-        l[e >> 1] += p[e];
-      }
-      pa[n >> 1][(n & 1) * 2] = X::pack(p[0], p[1]);
-      pa[n >> 1][(n & 1) * 2 + 1] = X::pack(p[2], p[3]);
-    }
-    const uint32_t vr = (lane & 7) + ((lane >> 3) & 1) * 8;
-#pragma unroll
-    for (int kk = 0; kk < KT / 16; ++kk)
-#pragma unroll
-      for (int n = 0; n < NO; n += 2) {
-        uint32_t vb[4];
-        ldsm4_t(vb, vd + row_chunk<D>(16 * kk + vr, n + (lane >> 4)));
-        X::mma(o[n], pa[kk], vb[0], vb[1]);
-        X::mma(o[n + 1], pa[kk], vb[2], vb[3]);
-      }
-    __syncthreads();
-  }
-  cp_async_wait<0>();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    const int r = 16 * warp + (lane >> 2) + 8 * h;
-    if (r >= rows) continue;
-    const int64_t f = row0 + r, row = (t0 + f / per) * a.hq + g * per + f % per;
-    const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
-#pragma unroll
-    for (int n = 0; n < NO; ++n)
-      *reinterpret_cast<uint32_t*>(a.out + row * D + 8 * n + 2 * (lane & 3)) =
-          X::pack(o[n][2 * h] * inv, o[n][2 * h + 1] * inv);
-    if (a.lse && (lane & 3) == 0)
-      a.lse[row] = l[h] == 0.f ? -INFINITY : (m[h] + log2f(l[h])) * 0.69314718055994531f;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
   }
 }
 
+// Joins the ranges of items whose keys were cut: one warp a query row.
 template <class E, int D>
-cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t s) {
-  static bool attr_done[64] = {false};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !attr_done[dev]) {
-    e = cudaFuncSetAttribute(paged_prefill_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem_bytes<D>());
-    if (e != cudaSuccess) return e;
-    if (dev < 64) attr_done[dev] = true;
+__global__ void __launch_bounds__(256) paged_prefill_join_kernel(const __grid_constant__ Args x) {
+  constexpr int W = D / 32;                         // dims of a lane: 2, 4 or 8
+  using X = Elem<E>;
+  const PagedAttnArgs& a = x.a;
+  pdl_wait();
+  const int64_t id = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5));
+  const int64_t w0 = id / M * x.grid.n_split;       // the item's first range
+  const int r = (int)(id % M), lane = threadIdx.x & 31;
+  if (w0 >= x.grid.n_slots * a.hk * x.grid.n_split) return;
+  const Item it(x, w0);
+  if (it.n_tiles <= 0 || it.pieces <= 1 || r >= it.rows) return;
+  const Scratch sc = scratch_of(a.scratch);
+  float m = -FLT_MAX, l = 0.f, acc[W];
+#pragma unroll
+  for (int e = 0; e < W; ++e) acc[e] = 0.f;
+  for (int i = 0; i < it.pieces; ++i) {
+    const int64_t row = (w0 + i) * M + r;
+    const float z = sc.lse2[row];
+    float v[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) v[e] = sc.o[row * D + W * lane + e];
+    if (z == -INFINITY) continue;                   // a range without a key
+    const float nm = fmaxf(m, z), f0 = exp2_approx(m - nm), f1 = exp2_approx(z - nm);
+    l = fmaf(l, f0, f1);
+#pragma unroll
+    for (int e = 0; e < W; ++e) acc[e] = fmaf(acc[e], f0, v[e] * f1);
+    m = nm;
   }
-  const int64_t slots = (a.T * (a.hq / a.hk) + ROWS - 1) / ROWS + a.B;
-  paged_prefill_kernel<E, D><<<dim3((unsigned)slots, a.hk), THREADS, smem_bytes<D>(), s>>>(a);
-  return cudaGetLastError();
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int per = a.hq / a.hk;
+  const int64_t flat = it.row0 + r, orow = (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + W * lane);
+#pragma unroll
+  for (int e = 0; e < W / 2; ++e) dst[e] = X::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+Grid grid_of(const PagedAttnArgs& a, int num_sms) {
+  Grid g;
+  g.n_slots = (a.T * (a.hq / a.hk) + M - 1) / M + a.B;
+  // ranges: as many as fill the SMs, from the slots (a sequence's last slot is
+  // often empty, so the SMs are filled to about a half at the least)
+  const int64_t n = (num_sms < MAX_PIECES ? num_sms : MAX_PIECES) / (g.n_slots * a.hk);
+  g.n_split = (int)(n < 1 ? 1 : (n > MAX_SPLIT ? MAX_SPLIT : n));
+  return g;
+}
+
+template <class E, int D>
+cudaError_t launch_d(const PagedAttnArgs& a, int num_sms, cudaStream_t s, bool join) {
+  Args x{a, grid_of(a, num_sms)};
+  const int64_t items = x.grid.n_slots * a.hk * x.grid.n_split;
+  if (!join) {
+    static bool attr_done[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !attr_done[dev]) {
+      e = cudaFuncSetAttribute(paged_prefill_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) attr_done[dev] = true;
+    }
+    paged_prefill_kernel<E, D><<<(int)(items < num_sms ? items : num_sms), THREADS, SMEM, s>>>(x);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items / x.grid.n_split * (M / 8)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<E, D>, x);
 }
 
 }  // namespace
 
-size_t paged_prefill_scratch(int) { return 0; }
+size_t paged_prefill_scratch(int head_dim) { return (size_t)MAX_PIECES * M * (head_dim + 1) * 4; }
 
-cudaError_t launch_paged_prefill(const PagedAttnArgs& a, int head_dim, int dtype, int, cudaStream_t s, bool join) {
-  if (a.B <= 0 || a.T <= 0 || join) return cudaSuccess;
+bool paged_prefill_splits(const PagedAttnArgs& a, int num_sms) { return grid_of(a, num_sms).n_split > 1; }
+
+cudaError_t launch_paged_prefill(const PagedAttnArgs& a, int head_dim, int dtype, int num_sms, cudaStream_t s,
+                                 bool join) {
+  if (a.B <= 0 || a.T <= 0) return cudaSuccess;
   const bool bf = dtype == QSA_DTYPE_BF16;
   switch (head_dim) {
-    case 64: return bf ? launch_d<__nv_bfloat16, 64>(a, s) : launch_d<__half, 64>(a, s);
-    case 128: return bf ? launch_d<__nv_bfloat16, 128>(a, s) : launch_d<__half, 128>(a, s);
-    case 256: return bf ? launch_d<__nv_bfloat16, 256>(a, s) : launch_d<__half, 256>(a, s);
+    case 64: return bf ? launch_d<__nv_bfloat16, 64>(a, num_sms, s, join) : launch_d<__half, 64>(a, num_sms, s, join);
+    case 128: return bf ? launch_d<__nv_bfloat16, 128>(a, num_sms, s, join) : launch_d<__half, 128>(a, num_sms, s, join);
+    case 256: return bf ? launch_d<__nv_bfloat16, 256>(a, num_sms, s, join) : launch_d<__half, 256>(a, num_sms, s, join);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -179,6 +179,7 @@ size_t paged_decode_scratch(int head_dim, int B);
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, int head_dim, int dtype, int num_sms, cudaStream_t s,
                                 bool join);
 size_t paged_prefill_scratch(int head_dim);
+bool paged_prefill_splits(const PagedAttnArgs& a, int num_sms);   // whether the join is due
 cudaError_t launch_paged_prefill(const PagedAttnArgs& a, int head_dim, int dtype, int num_sms, cudaStream_t s,
                                  bool join);
 
