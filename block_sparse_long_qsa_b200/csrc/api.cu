@@ -1139,7 +1139,7 @@ qsa_status check_kv(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B
   v.table_ld = kv->table_ld;
   v.n_pages = (int32_t)kv->n_pages;
   v.page_size = kv->page_size;
-  v.capacity = (int32_t)std::min<int64_t>(cap, INT32_MAX);
+  v.capacity = (int32_t)std::min<int64_t>(cap, (int64_t)1 << 30);   // key numbers stay in 32 bits
   // division by page_size: shift s with 2^s >= page_size, multiplier
   // floor(2^32 (2^s - page_size) / page_size) + 1
   uint32_t sh = 0;
@@ -1147,6 +1147,28 @@ qsa_status check_kv(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B
   v.div_shift = sh;
   v.div_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << sh) - (uint64_t)kv->page_size)) /
                              (uint64_t)kv->page_size + 1);
+  return QSA_OK;
+}
+
+// Pages as [n_pages][n_kv][page_size][head_dim] for TMA: boxes of `rows` rows of
+// a page x 64 dims, 128B swizzle.
+qsa_status make_map_pages(CUtensorMap* m, const qsa_layer_params* p, const qsa::PagedView& v, const uint16_t* base,
+                          int rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(QSA_ERR_CUDA, "cuTensorMapEncodeTiled entry point not found");
+  cuuint64_t dims[4] = {(cuuint64_t)p->head_dim, (cuuint64_t)v.page_size, (cuuint64_t)p->n_kv_heads,
+                        (cuuint64_t)v.n_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)v.token_stride * 2, (cuuint64_t)v.head_stride * 2, (cuuint64_t)v.page_stride * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, p->dtype == QSA_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<uint16_t*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char d[64];
+    std::snprintf(d, sizeof(d), "CUresult %d", (int)r);
+    return fail(QSA_ERR_CUDA, "cuTensorMapEncodeTiled", d);
+  }
   return QSA_OK;
 }
 
@@ -1344,13 +1366,18 @@ qsa_status qsa_paged_prefill(const qsa_layer_params* p, const qsa_paged_kv* kv, 
   a.err = static_cast<uint32_t*>(ws);
   a.scratch = static_cast<uint8_t*>(ws) + HEADER_BYTES;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CUtensorMap tk{}, tv{};
+  const int box = qsa::paged_prefill_box(a.kv.page_size);
+  if (box > 1 && ((st = make_map_pages(&tk, p, a.kv, a.kv.k, box)) != QSA_OK ||
+                  (st = make_map_pages(&tv, p, a.kv, a.kv.v, box)) != QSA_OK))
+    return st;
   if ((st = from_cuda(traced(QSA_KERNEL_PAGED_PREFILL, s, [&] {
-         return qsa::launch_paged_prefill(a, p->head_dim, p->dtype, di.num_sms, s, false);
+         return qsa::launch_paged_prefill(a, tk, tv, p->head_dim, p->dtype, di.num_sms, s, false);
        }), "paged prefill launch")) != QSA_OK)
     return st;
   if (!qsa::paged_prefill_splits(a, di.num_sms)) return QSA_OK;
   return from_cuda(traced(QSA_KERNEL_PAGED_PREFILL_JOIN, s, [&] {
-    return qsa::launch_paged_prefill(a, p->head_dim, p->dtype, di.num_sms, s, true);
+    return qsa::launch_paged_prefill(a, tk, tv, p->head_dim, p->dtype, di.num_sms, s, true);
   }), "paged prefill join launch");
 }
 

@@ -62,11 +62,9 @@ struct Visible {
   int n, ns, lo;
   __device__ __forceinline__ Visible(const PagedAttnArgs& a, int L, uint32_t* err) {
     if (L < 0) { n = ns = lo = 0; return; }
-    int end = L + 1;
-    if (L >= a.kv.capacity) {                     // past the table: what it holds
-      report_error(err, QSA_ERR_DEVICE_BOUNDS);
-      end = a.kv.capacity;
-    }
+    const bool past = L >= a.kv.capacity;         // past the table: what it holds
+    const int end = past ? a.kv.capacity : L + 1;
+    if (past) report_error(err, QSA_ERR_DEVICE_BOUNDS);
     lo = a.window > 0 && L >= a.window ? L - a.window + 1 : 0;
     if (lo > end) lo = end;
     ns = a.sinks < lo ? a.sinks : lo;

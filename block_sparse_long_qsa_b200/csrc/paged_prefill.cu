@@ -17,10 +17,15 @@
 //     their tile maxima; it is raised only when a tile exceeds it by more than
 //     8, so the rescale of O is rare), exp2, P packed to 16 bits into the score
 //     buffer; at the end O / l and the log-sum-exp.
-//   * warps 8-11 (loaders): the Q tile, then K and V by cp.async, 16 bytes a
-//     thread, rows found through the page table, rows that no query sees zero.
-//     Slots of 16 KB in one ring: K as 128 keys x 64 dims, V as 128 * 64 / D
-//     keys x D dims, in the order the products take them.
+//   * warps 8-11 (loaders): the Q tile, then K and V.  Slots of 16 KB in one
+//     ring: K as 128 keys x 64 dims, V as 128 * 64 / D keys x D dims, in the
+//     order the products take them.  Where the page size is a multiple of 16,
+//     warp 8 fetches them by TMA, a box of 16 or 32 rows of a page x 64 dims at
+//     a time (the numbering of the keys is rounded so that no box crosses a
+//     page); a V slot with rows that no query sees, whose memory may hold
+//     anything, is copied by all four warps with cp.async and zeros in place of
+//     those rows.  Other page sizes go by cp.async row by row.  (K rows that
+//     nobody sees need no care: their scores are replaced.)
 //   * warp 12 (one thread): S(i + 1) = Q K^T (M = 128, N = 128) is issued before
 //     O += P V (N = D) of tile i, so the tensor cores work on one while the
 //     softmax makes the other's operand.
@@ -46,7 +51,7 @@ constexpr int LWARPS = 4;                           // loader warps (more leave 
 constexpr int W_LOAD = 8, W_MMA = W_LOAD + LWARPS;
 constexpr int LOADERS = 32 * LWARPS;
 constexpr int THREADS = 32 * (W_MMA + 1);
-constexpr int RT = LOADERS / 8, RJ = KT / RT;       // rows of a loader pass, passes of a tile
+constexpr int RT = LOADERS / 8, RJ = KT / RT;       // cp.async: rows of a pass, passes of a tile
 constexpr uint32_t SLOT = 16384;
 constexpr int NS = 10;                              // slots of the ring
 constexpr uint32_t OFF_RING = 65536;                // Q: up to 128 rows x 512 B
@@ -68,8 +73,18 @@ __device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t c16) {
   return row * 128u + ((c16 ^ (row & 7u)) << 4);
 }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+// The barrier's phase waits for this thread's copies so far, beside its counted
+// arrivals (this form adds the arrival that it makes to the pending count).
+__device__ __forceinline__ void cp_async_hold(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// A box of a page: dims, rows of the page, KV head, page (no multicast).
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* m, int32_t dim, int32_t row, int32_t head,
+                                             int32_t page, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(dim), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
 }
 // MN-major operand descriptor (128-byte swizzle): lbo = distance between
 // 64-element atoms along N, sbo = distance between 8-row groups along K.
@@ -87,16 +102,28 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
       ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -113,8 +140,10 @@ __host__ __device__ inline Scratch scratch_of(void* p) {
 }
 
 struct Args {
+  CUtensorMap tk, tv;       // TMA: boxes of `box` rows x 64 dims
   PagedAttnArgs a;
   Grid grid;
+  int box;                  // 16 or 32, or 1: no TMA
 };
 
 // Item w.  Sequence b owns the tile slots from cu[b] per / 128 + b on (at least
@@ -124,7 +153,8 @@ struct Item {
   int b, g, rows;           // sequence, KV head, rows in use
   int n_tiles, tile0;       // tiles of this range, its first
   int pieces, split;        // ranges that the item's keys are cut into, which one this is
-  int lo, ns, n_vis;        // visible key v: v < ns ? v : lo + v - ns
+  int lo, ns, n_vis;        // key number v: v < ns ? v : lo + v - ns (whole boxes)
+  int first, end;           // keys needed: [first, end) and those below the sinks
   int p0;                   // position of the first row's token
   int64_t t0, row0;         // the sequence's first token row; first flat row of the item
   __device__ __forceinline__ Item(const Args& x, int64_t w) {
@@ -149,13 +179,15 @@ struct Item {
     row0 = tile * M;
     rows = (int)min((int64_t)M, n_rows - row0);
     if (t0 < 0 || tile < 0 || rows <= 0 || L < 0) return;
-    const int64_t first = L + row0 / per, last = L + (row0 + rows - 1) / per;
-    const int end = (int)min(last + 1, (int64_t)a.kv.capacity);
+    const int64_t pos = L + row0 / per, last = L + (row0 + rows - 1) / per;
+    end = (int)min(last + 1, (int64_t)a.kv.capacity);
     if (last >= a.kv.capacity) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
-    lo = a.window > 0 && first >= a.window ? (int)min(first - a.window + 1, (int64_t)end) : 0;
-    ns = min(a.sinks, lo);
+    first = a.window > 0 && pos >= a.window ? (int)min(pos - a.window + 1, (int64_t)end) : 0;
+    lo = first / x.box * x.box;
+    ns = min((a.sinks + x.box - 1) / x.box * x.box, lo);
+    if (ns == lo) ns = lo = 0;                      // no gap
     n_vis = ns + end - lo;
-    p0 = (int)min(first, (int64_t)INT32_MAX);
+    p0 = (int)min(pos, (int64_t)INT32_MAX);
     // at least one tile: rows whose keys all lie past the table come out zero
     const int all = max((n_vis + KT - 1) / KT, 1), each = (all + ns_ - 1) / ns_;
     pieces = (all + each - 1) / each;
@@ -164,7 +196,7 @@ struct Item {
   }
 };
 
-template <class E, int D>
+template <class E, int D, bool TMA>
 __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_constant__ Args x) {
   constexpr int NCH = D / 64;                       // 64-dim chunks: K (and V) slots of a tile
   constexpr int KV = KT / NCH;                      // keys of a V slot
@@ -194,12 +226,12 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     return;
   }
   if (tid == 0) {
-    for (int s = 0; s < NS; ++s) { mbar_init(&full[s], LOADERS); mbar_init(&empty[s], 1); }
-    mbar_init(q_full, LOADERS);
+    for (int s = 0; s < NS; ++s) { mbar_init(&full[s], LWARPS); mbar_init(&empty[s], 1); }
+    mbar_init(q_full, LWARPS);
     mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8); mbar_init(&pv_done[i], 1); }
     mbar_init(o_empty, 8);
-    for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 64);
+    for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 2);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -215,74 +247,169 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
 
   if (warp >= W_LOAD && warp < W_MMA) {
     // ---------------------------------------------------------------- loaders
-    const int lt = tid - 32 * W_LOAD, c = lt & 7, rt = lt >> 3;   // 16-byte chunk, row of a pass
+    const int lt = tid - 32 * W_LOAD, c = lt & 7, rt = lt >> 3;   // cp.async: 16-byte chunk, row of a pass
+    const int lw = warp - W_LOAD;
     int slot = 0;
     uint32_t eph = 1, items_done = 0, count = 0;   // tiles so far
+    uint32_t landing = 0;                          // slots with a TMA copy that the MMA may not have seen
     bool ok = true;
+    // one arrival per warp, after its lanes' copies are on their way; bytes: what
+    // the warp fetches by TMA
+    auto arrive = [&](uint64_t* bar, uint32_t bytes) {
+      __syncwarp();
+      if (lane == 0) {
+        if (bytes) mbar_arrive_expect_tx(bar, bytes);
+        else mbar_arrive(bar);
+      }
+    };
     auto advance = [&]() { if (++slot == NS) { slot = 0; eph ^= 1; } };
     for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
       const Item it(x, w);
       if (it.n_tiles <= 0) continue;
       const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
       const int64_t head = (int64_t)it.g * a.kv.head_stride + 8 * c;
-      // this thread's rows rt + RT j of a tile, for K and V alike: offset of its
-      // chunk of the row, or -1
-      int64_t off_k[RJ], off_v[RJ];
-      auto find_rows = [&](int tile) {
+      auto key_of = [&](int v) { return v < it.ns ? v : it.lo + (v - it.ns); };
+      auto needed = [&](int key) { return key < it.end && (key >= it.first || key < a.sinks); };
+      // ---- by boxes (TMA): lane i of each warp knows box i of a tile
+      const int box = x.box, nb = KT / box, bs = box == 32 ? 5 : 4;   // box = 1 << bs
+      struct Box { int id, row; bool good, clean; };  // page, first row in it; there at all; every row needed
+      auto find_box = [&](int tile) -> Box {
+        const int key = key_of(tile * KT + (lane & (nb - 1)) * box);
+        // some row of the box is needed: its last row, or the first of those left by the sinks
+        const bool any = key < it.end && (key + box > it.first || key < a.sinks);
+        Box r;
+        r.id = any ? __ldg(table + page_of(a.kv, (uint32_t)key)) : -1;
+        r.good = (uint32_t)r.id < (uint32_t)a.kv.n_pages;
+        if (any && !r.good) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
+        r.row = key - (int)(page_of(a.kv, (uint32_t)key) * (uint32_t)a.kv.page_size);
+        r.clean = r.good && key + box <= it.end && (key >= it.first || key + box <= a.sinks);
+        return r;
+      };
+      // ---- row by row: this thread's rows rt + RT j of a tile, the page ids
+      // loaded a tile ahead, all at once
+      int32_t ids[RJ];
+      auto load_ids = [&](int tile) {
 #pragma unroll
         for (int j = 0; j < RJ; ++j) {
-          const int v = tile * KT + RT * j + rt;
-          off_k[j] = -1;
-          if (v < it.n_vis) {
-            const int64_t o = page_row(a.kv, table, v < it.ns ? v : it.lo + (v - it.ns), a.err);
-            if (o >= 0) off_k[j] = o + head;
-          }
-          // the warp's four rows of the pass: one byte of their bits
-          const uint32_t bits = __ballot_sync(0xffffffffu, off_k[j] >= 0 && c == 0);
-          if (lane == 0) {
-            const uint32_t four = (bits & 1) | (bits >> 7 & 2) | (bits >> 14 & 4) | (bits >> 21 & 8);
-            reinterpret_cast<volatile uint8_t*>(rows_ok)[(count % NOK) * 32 + j * LWARPS + (warp - W_LOAD)] = (uint8_t)four;
-          }
+          const int key = key_of(min(tile * KT + RT * j + rt, it.n_vis - 1));
+          ids[j] = __ldg(table + page_of(a.kv, (uint32_t)max(key, 0)));
         }
       };
-      auto load_k = [&]() -> bool {
+      auto row_off = [&](int key, int id) -> int64_t {
+        const int in_page = key - (int)(page_of(a.kv, (uint32_t)key) * (uint32_t)a.kv.page_size);
+        return (int64_t)id * a.kv.page_stride + (int64_t)in_page * a.kv.token_stride + head;
+      };
+      Box bk{}, bv{}, bn{};                          // boxes of the K tile, the V tile, the next K tile
+      int64_t off_k[TMA ? 1 : RJ], off_v[TMA ? 1 : RJ];
+      if (TMA) bn = find_box(it.tile0);
+      else load_ids(it.tile0);
+      auto begin_tile = [&](int tile) {
+        const uint32_t at = (count % NOK) * 32;
+        if constexpr (TMA) {
+          bk = bn;
+          const uint32_t good = __ballot_sync(0xffffffffu, bk.good);
+          if (lw == 0) reinterpret_cast<volatile uint8_t*>(rows_ok)[at + lane] = (good >> ((4 * lane) >> bs)) & 1 ? 15 : 0;
+          bn = find_box(tile + 1);
+        } else {
 #pragma unroll
+          for (int j = 0; j < RJ; ++j) {
+            const int v = tile * KT + RT * j + rt;
+            const bool there = v < it.n_vis, good = there && (uint32_t)ids[j] < (uint32_t)a.kv.n_pages;
+            if (there && !good) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
+            off_k[j] = good ? row_off(key_of(v), ids[j]) : -1;
+            // the warp's four rows of the pass: one byte of their bits
+            const uint32_t bits = __ballot_sync(0xffffffffu, good && c == 0);
+            if (lane == 0) {
+              const uint32_t four = (bits & 1) | (bits >> 7 & 2) | (bits >> 14 & 4) | (bits >> 21 & 8);
+              reinterpret_cast<volatile uint8_t*>(rows_ok)[at + j * LWARPS + lw] = (uint8_t)four;
+            }
+          }
+          load_ids(tile + 1);
+        }
+        ++count;
+      };
+      auto load_k = [&]() -> bool {
         for (int ch = 0; ch < NCH; ++ch) {
           if (!mbar_wait(&empty[slot], eph, abort_flag, a.err)) return false;
           const uint32_t dst = smem_u32(smem + OFF_RING + slot * SLOT);
+          if constexpr (TMA) {
+            uint32_t bytes = 0;
+            if (lw == 0) {
+              const bool mine = lane < nb && bk.good;
+              bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box * 128;
+              if (bytes) landing |= 1u << slot;
+              arrive(&full[slot], bytes);
+              if (mine) tma_load_box(dst + lane * box * 128, &x.tk, 64 * ch, bk.row, it.g, bk.id, &full[slot]);
+            } else {
+              arrive(&full[slot], 0);
+            }
+          } else {
 #pragma unroll
-          for (int j = 0; j < RJ; ++j) {
-            const bool valid = off_k[j] >= 0;
-            cp_async16_zfill(dst + swz128(RT * j + rt, c), valid ? a.kv.k + off_k[j] + 64 * ch : a.kv.k, valid);
+            for (int j = 0; j < RJ; ++j) {
+              const bool valid = off_k[j] >= 0;
+              cp_async16_zfill(dst + swz128(RT * j + rt, c), valid ? a.kv.k + off_k[j] + 64 * ch : a.kv.k, valid);
+            }
+            cp_async_hold(&full[slot]);
+            arrive(&full[slot], 0);
           }
-          cp_async_arrive(&full[slot]);
           advance();
         }
         return true;
       };
-      auto load_v = [&]() -> bool {
+      auto load_v = [&](int tile) -> bool {
 #pragma unroll
         for (int s = 0; s < NCH; ++s) {
           if (!mbar_wait(&empty[slot], eph, abort_flag, a.err)) return false;
           const uint32_t dst = smem_u32(smem + OFF_RING + slot * SLOT);
+          if constexpr (TMA) {
+            const int b0 = s * KV >> bs, n = KV >> bs;   // the slot's boxes
+            const uint32_t clean = __ballot_sync(0xffffffffu, bv.clean) >> b0;
+            if ((~clean & ((1u << n) - 1)) == 0) {
+              const int i = lane / NCH, ch = lane % NCH;
+              const int id = __shfl_sync(0xffffffffu, bv.id, (b0 + i) & 31), row = __shfl_sync(0xffffffffu, bv.row, (b0 + i) & 31);
+              if (lw == 0) {
+                landing |= 1u << slot;
+                arrive(&full[slot], SLOT);
+                if (i < n)                            // n NCH is 4 or 8
+                  tma_load_box(dst + ch * (KV * 128) + i * box * 128, &x.tv, 64 * ch, row, it.g, id, &full[slot]);
+              } else {
+                arrive(&full[slot], 0);
+              }
+              advance();
+              continue;
+            }
 #pragma unroll
-          for (int j = 0; j < KV / RT; ++j) {
-            const int64_t o = off_v[s * (KV / RT) + j];
-            const bool valid = o >= 0;
+            for (int j = 0; j < KV / RT; ++j) {
+              const int r = s * KV + RT * j + rt, from = r >> bs;
+              const int key = key_of(tile * KT + r);
+              const int id = __shfl_sync(0xffffffffu, bv.id, from);
+              const bool valid = needed(key) && (uint32_t)id < (uint32_t)a.kv.n_pages;
+              const int64_t o = valid ? row_off(key, id) : 0;
 #pragma unroll
-            for (int ch = 0; ch < NCH; ++ch)
-              cp_async16_zfill(dst + ch * (KV * 128) + swz128(RT * j + rt, c), valid ? a.kv.v + o + 64 * ch : a.kv.v,
-                               valid);
+              for (int ch = 0; ch < NCH; ++ch)
+                cp_async16_zfill(dst + ch * (KV * 128) + swz128(RT * j + rt, c), valid ? a.kv.v + o + 64 * ch : a.kv.v,
+                                 valid);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < KV / RT; ++j) {
+              const int64_t o = off_v[s * (KV / RT) + j];
+              const bool valid = o >= 0;
+#pragma unroll
+              for (int ch = 0; ch < NCH; ++ch)
+                cp_async16_zfill(dst + ch * (KV * 128) + swz128(RT * j + rt, c), valid ? a.kv.v + o + 64 * ch : a.kv.v,
+                                 valid);
+            }
           }
-          cp_async_arrive(&full[slot]);
+          cp_async_hold(&full[slot]);
+          arrive(&full[slot], 0);
           advance();
         }
         return true;
       };
       for (int i = 0; ok && i <= it.n_tiles; ++i) {
         if (i < it.n_tiles) {
-          find_rows(it.tile0 + i);
-          ++count;
+          begin_tile(it.tile0 + i);
           if (!load_k()) { ok = false; break; }
         }
         if (i == 0) {
@@ -298,17 +425,28 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
             for (int ch = 0; ch < NCH; ++ch)
               cp_async16_zfill(smem_u32(smem + ch * SLOT) + swz128(r, c), valid ? src + 64 * ch : a.q, valid);
           }
-          cp_async_arrive(q_full);
-        } else if (!load_v()) {
+          cp_async_hold(q_full);
+          arrive(q_full, 0);
+        } else if (!load_v(it.tile0 + i - 1)) {
           ok = false;
           break;
         }
+        if constexpr (TMA) {
+          bv = bk;
+        } else {
 #pragma unroll
-        for (int j = 0; j < RJ; ++j) off_v[j] = off_k[j];
+          for (int j = 0; j < RJ; ++j) off_v[j] = off_k[j];
+        }
       }
       ++items_done;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    // After an abort no TMA copy may still be writing when the CTA exits: wait
+    // for the last phase of every slot that one went to (without an abort the
+    // MMA has waited for all of them, and these return at once).
+    if (TMA && lw == 0 && lane == 0)
+      for (int s = 0; s < NS; ++s)
+        if (landing >> s & 1) mbar_wait_drain(&full[s], (s < slot ? eph : eph ^ 1) ^ 1, a.err);
   } else if (warp == W_MMA) {
     // -------------------------------------------------------------------- MMA
     if (lane == 0) {
@@ -389,27 +527,38 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     auto exchange = [&](float mine, float& other) -> bool {
       const uint32_t s = (xc & 1) * 2;
       xch[(s + half) * M + r] = mine;
-      mbar_arrive(&xbar[quad]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&xbar[quad]);
       const bool okx = __all_sync(0xffffffffu, mbar_wait(&xbar[quad], xc & 1, abort_flag, a.err));
       other = xch[(s + (half ^ 1)) * M + r];
       ++xc;
       return okx;
     };
     for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
-      const Item it(x, w);
-      if (it.n_tiles <= 0) continue;
-      const bool in = r < it.rows;
-      const int64_t flat = it.row0 + (in ? r : 0);
-      // the row sees v in [v_min, v_max] and v < sinks (in the numbering without the gap)
-      const int64_t pos = (int64_t)it.p0 + (flat / per - it.row0 / per);
-      const int v_max = (int)min(pos - it.lo + it.ns, (int64_t)it.n_vis - 1);
-      const int v_min = a.window > 0 ? (int)max(pos - a.window + 1 - it.lo + it.ns, (int64_t)0) : 0;
-      // the whole item's: every row sees v in [all_min, all_max]
-      const int64_t pos1 = (int64_t)it.p0 + ((it.row0 + it.rows - 1) / per - it.row0 / per);
-      const int all_max = (int)min((int64_t)it.p0 - it.lo + it.ns, (int64_t)it.n_vis - 1);
-      const int all_min = a.window > 0 ? (int)max(pos1 - a.window + 1 - it.lo + it.ns, (int64_t)0) : 0;
+      int n_tiles, v0;                                // tiles of the item, first key number of the tile
+      int v_min, v_max;                               // the row sees v in [v_min, v_max] and v < sinks
+      int all_min, all_max;                           // every row sees v in [all_min, all_max]
+      int64_t orow;                                   // output row, or piece row; -1: row not in use
+      bool part;
+      {
+        const Item it(x, w);
+        if (it.n_tiles <= 0) continue;
+        n_tiles = it.n_tiles;
+        v0 = it.tile0 * KT;
+        const bool in = r < it.rows;
+        const int64_t flat = it.row0 + (in ? r : 0), tok0 = it.row0 / per;
+        const int shift = it.ns - it.lo;              // position -> number, behind the gap
+        const int64_t pos = (int64_t)it.p0 + (flat / per - tok0);
+        const int64_t pos1 = (int64_t)it.p0 + ((it.row0 + it.rows - 1) / per - tok0);
+        v_max = (int)min(pos + shift, (int64_t)it.n_vis - 1);
+        all_max = (int)min((int64_t)it.p0 + shift, (int64_t)it.n_vis - 1);
+        v_min = a.window > 0 ? (int)max(pos - a.window + 1 + shift, (int64_t)0) : 0;
+        all_min = a.window > 0 ? (int)max(pos1 - a.window + 1 + shift, (int64_t)0) : 0;
+        part = it.pieces > 1;
+        orow = !in ? -1 : part ? w * M + r : (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
+      }
       float m = -FLT_MAX, l = 0.f;
-      for (int i = 0; i < it.n_tiles; ++i, ++count) {
+      for (int i = 0; i < n_tiles; ++i, ++count, v0 += KT) {
         const uint32_t buf = count & 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], (count >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
         tc_fence_after();
@@ -417,28 +566,32 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
         float s0[32], s1[32];
         tmem_ld32(s_addr + 64 * half, s0);
         tmem_ld32(s_addr + 64 * half + 32, s1);
+        // the keys that are there, four to a byte
+        const uint4 there = *reinterpret_cast<const uint4*>(smem + OFF_OK + (count % NOK) * 32 + 16 * half);
+        const bool whole = v0 + KT - 1 <= all_max && (v0 >= all_min || v0 + KT <= a.sinks) &&
+                           (there.x & there.y & there.z & there.w) == 0x0f0f0f0fu;
         tmem_ld_wait(s0);
         tmem_ld_wait(s1);
-        const int v0 = (it.tile0 + i) * KT;
-        // the keys that are there, four to a byte
-        const uint64_t w0 = rows_ok[(count % NOK) * 4 + 2 * half], w1 = rows_ok[(count % NOK) * 4 + 2 * half + 1];
-        const bool whole = v0 + KT - 1 <= all_max && (v0 >= all_min || v0 + KT <= a.sinks) &&
-                           (w0 & w1) == 0x0f0f0f0f0f0f0f0full;
         if (!whole) {
           const int vb = v0 + 64 * half;
+          const uint32_t bits[4] = {there.x, there.y, there.z, there.w};
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int va = vb + e, vc = va + 32;
-            const bool oka = va <= v_max && (va >= v_min || va < a.sinks) && (w0 >> ((e >> 2) * 8 + (e & 3)) & 1);
-            const bool okc = vc <= v_max && (vc >= v_min || vc < a.sinks) && (w1 >> ((e >> 2) * 8 + (e & 3)) & 1);
+            const bool oka = va <= v_max && (va >= v_min || va < a.sinks) && (bits[e >> 4] >> ((e >> 2 & 3) * 8 + (e & 3)) & 1);
+            const bool okc = vc <= v_max && (vc >= v_min || vc < a.sinks) && (bits[2 + (e >> 4)] >> ((e >> 2 & 3) * 8 + (e & 3)) & 1);
             if (!oka) s0[e] = -INFINITY;
             if (!okc) s1[e] = -INFINITY;
           }
         }
-        float mt = -INFINITY;
+        float mt = max3f(s0[0], s1[0], s0[1]), mu = max3f(s1[1], s0[2], s1[2]);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) mt = max3f(mt, s0[e], s1[e]);
-        mt = fmaxf(mt * a.scale_log2, -FLT_MAX);    // a tile without a key leaves the maximum as it is
+        for (int e = 3; e + 1 < 32; e += 2) {
+          mt = max3f(mt, s0[e], s1[e]);
+          mu = max3f(mu, s0[e + 1], s1[e + 1]);
+        }
+        mt = max3f(mt, s0[31], s1[31]);
+        mt = fmaxf(fmaxf(mt, mu) * a.scale_log2, -FLT_MAX);   // a tile without a key leaves the maximum as it is
         float other;
         if (!exchange(mt, other)) { ok = false; break; }
         mt = fmaxf(mt, other);
@@ -455,36 +608,38 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
             if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[g & 1], (g >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < D / 64; ++cc) {
-              float o[32];
-              const uint32_t ad = tmem + lanes + TM_O + (D / 2) * half + 32 * cc;
-              tmem_ld32(ad, o);
-              tmem_ld_wait(o);
-              uint32_t u[32];
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t o[16];
+              const uint32_t ad = tmem + lanes + TM_O + (D / 2) * half + 16 * cc;
+              tmem_ld16(ad, o);                     // waits for the load
 #pragma unroll
-              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
-              tmem_st32(ad, u);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(ad, o);
             }
             tmem_st_wait();
           }
         }
         // p = 2^(s scale - m); the sum takes the fp32 values, the products p rounded to 16 bits
-        uint32_t pk[32];
-        float l0 = 0.f, l1 = 0.f;
-        const float nm = -m;
+        const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-m, -m);
+        uint64_t sum = pk2(0.f, 0.f);
+        uint32_t pk[16];
+        auto exps = [&](const float (&sv)[32], uint32_t addr) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float a0 = exp2_approx(fmaf(s0[2 * e], a.scale_log2, nm));
-          const float a1 = exp2_approx(fmaf(s0[2 * e + 1], a.scale_log2, nm));
-          const float b0 = exp2_approx(fmaf(s1[2 * e], a.scale_log2, nm));
-          const float b1 = exp2_approx(fmaf(s1[2 * e + 1], a.scale_log2, nm));
-          l0 += a0 + a1;
-          l1 += b0 + b1;
-          pk[e] = X::pack(a0, a1);
-          pk[16 + e] = X::pack(b0, b1);
-        }
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            upk2(fma2(pk2(sv[2 * e], sv[2 * e + 1]), sc2, nm2), x0, x1);
+            x0 = exp2_approx(x0);
+            x1 = exp2_approx(x1);
+            sum = add2(sum, pk2(x0, x1));
+            pk[e] = X::pack(x0, x1);
+          }
+          tmem_st16(addr, pk);
+        };
+        exps(s0, s_addr + 32 * half);
+        exps(s1, s_addr + 32 * half + 16);
+        float l0, l1;
+        upk2(sum, l0, l1);
         l += l0 + l1;
-        tmem_st32(s_addr + 32 * half, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -500,22 +655,19 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       const float lr = l + l_other;
       const float inv = lr == 0.f ? 0.f : 1.f / lr;   // no key at all: zero
       const float lse2 = lr == 0.f ? -INFINITY : m + log2f(lr);
-      const int64_t orow = (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
-      const bool part = it.pieces > 1;
       const Scratch sc = scratch_of(a.scratch);
-      const int64_t prow = w * M + r;
 #pragma unroll 1
       for (int cc = 0; cc < D / 64; ++cc) {
         float o[32];
         const int d0 = (D / 2) * half + 32 * cc;
         tmem_ld32(tmem + lanes + TM_O + d0, o);
         tmem_ld_wait(o);
-        if (in && part) {
-          float4* dst = reinterpret_cast<float4*>(sc.o + prow * D + d0);
+        if (orow >= 0 && part) {
+          float4* dst = reinterpret_cast<float4*>(sc.o + orow * D + d0);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             dst[q] = make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv, o[4 * q + 3] * inv);
-        } else if (in) {
+        } else if (orow >= 0) {
           uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + d0);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -524,8 +676,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
                                 X::pack(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
         }
       }
-      if (in && half == 0) {
-        if (part) sc.lse2[prow] = lse2;
+      if (orow >= 0 && half == 0) {
+        if (part) sc.lse2[orow] = lse2;
         else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
       }
       tc_fence_before();
@@ -591,22 +743,34 @@ Grid grid_of(const PagedAttnArgs& a, int num_sms) {
   return g;
 }
 
+template <class E, int D, bool TMA>
+cudaError_t launch_attn(const Args& x, int grid, cudaStream_t s) {
+  static bool attr_done[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !attr_done[dev]) {
+    e = cudaFuncSetAttribute(paged_prefill_kernel<E, D, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_done[dev] = true;
+  }
+  paged_prefill_kernel<E, D, TMA><<<grid, THREADS, SMEM, s>>>(x);
+  return cudaGetLastError();
+}
+
 template <class E, int D>
-cudaError_t launch_d(const PagedAttnArgs& a, int num_sms, cudaStream_t s, bool join) {
-  Args x{a, grid_of(a, num_sms)};
+cudaError_t launch_d(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t s,
+                     bool join) {
+  Args x;
+  x.tk = tk;
+  x.tv = tv;
+  x.a = a;
+  x.grid = grid_of(a, num_sms);
+  x.box = paged_prefill_box(a.kv.page_size);
   const int64_t items = x.grid.n_slots * a.hk * x.grid.n_split;
   if (!join) {
-    static bool attr_done[64] = {false};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64 || !attr_done[dev]) {
-      e = cudaFuncSetAttribute(paged_prefill_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
-      if (e != cudaSuccess) return e;
-      if (dev < 64) attr_done[dev] = true;
-    }
-    paged_prefill_kernel<E, D><<<(int)(items < num_sms ? items : num_sms), THREADS, SMEM, s>>>(x);
-    return cudaGetLastError();
+    const int grid = (int)(items < num_sms ? items : num_sms);
+    return x.box > 1 ? launch_attn<E, D, true>(x, grid, s) : launch_attn<E, D, false>(x, grid, s);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items / x.grid.n_split * (M / 8)));
@@ -626,14 +790,19 @@ size_t paged_prefill_scratch(int head_dim) { return (size_t)MAX_PIECES * M * (he
 
 bool paged_prefill_splits(const PagedAttnArgs& a, int num_sms) { return grid_of(a, num_sms).n_split > 1; }
 
-cudaError_t launch_paged_prefill(const PagedAttnArgs& a, int head_dim, int dtype, int num_sms, cudaStream_t s,
-                                 bool join) {
+int paged_prefill_box(int page_size) { return page_size % 32 == 0 ? 32 : (page_size % 16 == 0 ? 16 : 1); }
+
+cudaError_t launch_paged_prefill(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
+                                 int dtype, int num_sms, cudaStream_t s, bool join) {
   if (a.B <= 0 || a.T <= 0) return cudaSuccess;
   const bool bf = dtype == QSA_DTYPE_BF16;
   switch (head_dim) {
-    case 64: return bf ? launch_d<__nv_bfloat16, 64>(a, num_sms, s, join) : launch_d<__half, 64>(a, num_sms, s, join);
-    case 128: return bf ? launch_d<__nv_bfloat16, 128>(a, num_sms, s, join) : launch_d<__half, 128>(a, num_sms, s, join);
-    case 256: return bf ? launch_d<__nv_bfloat16, 256>(a, num_sms, s, join) : launch_d<__half, 256>(a, num_sms, s, join);
+    case 64: return bf ? launch_d<__nv_bfloat16, 64>(a, tk, tv, num_sms, s, join)
+                        : launch_d<__half, 64>(a, tk, tv, num_sms, s, join);
+    case 128: return bf ? launch_d<__nv_bfloat16, 128>(a, tk, tv, num_sms, s, join)
+                        : launch_d<__half, 128>(a, tk, tv, num_sms, s, join);
+    case 256: return bf ? launch_d<__nv_bfloat16, 256>(a, tk, tv, num_sms, s, join)
+                        : launch_d<__half, 256>(a, tk, tv, num_sms, s, join);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -382,7 +382,7 @@ qsa_status qsa_decode_noalloc_check_error(void* stream);
  *     until the next qsa_check_device_error.  Calls that overlap on the GPU
  *     need a workspace each.
  *   - Device-side checks: a page id outside [0, n_pages), and a position past
- *     the table, record QSA_ERR_DEVICE_BOUNDS; the tokens there are left out
+ *     the table (or past 2^30), record QSA_ERR_DEVICE_BOUNDS; the tokens there are left out
  *     (not written by the append, masked in the attention).  Only entries of
  *     pages that hold a needed token are read, so entries of pages given back
  *     behind a window may hold anything. */

@@ -118,7 +118,7 @@ def test_call_checks():
     assert call("append", p, T=1 << 24) == UNSUPPORTED
     assert call("decode", p, q=None) == INVALID
     assert call("decode", p, out=A + 8) == MISALIGNED
-    assert call("decode", p, kv_struct(max_pages=1 << 20, table_ld=1 << 20, page_size=65536), B=64) == UNSUPPORTED
+    assert call("decode", p, kv_struct(max_pages=1 << 20, table_ld=1 << 20, page_size=65536), B=65) == UNSUPPORTED
     assert call("prefill", p, cu=None) == INVALID
     assert call("prefill", p, T=-1) == INVALID
     assert call("prefill", p, T=1 << 24) == UNSUPPORTED
