@@ -13,22 +13,25 @@
 // and taken in tiles of 128.  Persistent CTAs (one per SM) walk the items, those
 // of the last tokens (the most keys) first.
 //   * warps 0-7 (softmax): two threads a query row (TMEM lane), each with half
-//     of a tile's 128 scores: mask, running maximum in base 2 (the halves swap
-//     their tile maxima; it is raised only when a tile exceeds it by more than
-//     8, so the rescale of O is rare), exp2, P packed to 16 bits into the score
-//     buffer; at the end O / l and the log-sum-exp.
-//   * warps 8-11 (loaders): the Q tile, then K and V.  Slots of 16 KB in one
-//     ring: K as 128 keys x 64 dims, V as 128 * 64 / D keys x D dims, in the
-//     order the products take them.  Where the page size is a multiple of 16,
-//     warp 8 fetches them by TMA, a box of 16 or 32 rows of a page x 64 dims at
-//     a time (the numbering of the keys is rounded so that no box crosses a
-//     page); a V slot with rows that no query sees, whose memory may hold
-//     anything, is copied by all four warps with cp.async and zeros in place of
-//     those rows.  Other page sizes go by cp.async row by row.  (K rows that
-//     nobody sees need no care: their scores are replaced.)
+//     of a tile's 128 scores: mask, exp2 under the running maximum of the tiles
+//     before (base 2), P packed to 16 bits into the score buffer.  Meanwhile the
+//     halves swap their tile maxima; only a tile that exceeds the running one by
+//     more than 8 raises it, rescales O and is taken again.  At the end O / l and
+//     the log-sum-exp.
+//   * warp 13 (K): slots of 128 keys x 64 dims by TMA, a box of 16 to 64 rows of
+//     a page at a time (the numbering of the keys is rounded so that no box
+//     crosses a page).  K rows that nobody sees need no care: their scores are
+//     replaced.
+//   * warps 8-11 (V): the Q tile, then slots of 128 * 64 / D keys x D dims by
+//     cp.async, 16 bytes a thread; rows that no query sees, whose memory may hold
+//     anything, are zero.  Page sizes that are no multiple of 16 have K this way
+//     too.  K by one engine and V by the other because neither feeds the tensor
+//     cores alone: a TMA box takes 52 + 3.2 cycles a row of 128 bytes (at most 40
+//     bytes a cycle), four warps of cp.async bring 32.
 //   * warp 12 (one thread): S(i + 1) = Q K^T (M = 128, N = 128) is issued before
 //     O += P V (N = D) of tile i, so the tensor cores work on one while the
 //     softmax makes the other's operand.
+// Registers: 168 a softmax thread, 88 the others (setmaxnreg).
 // Every mbarrier wait is bounded (timeout -> error word, clean exit): on an abort
 // every role leaves its loop, the loaders wait for their own copies and the MMA
 // thread for its last commit before TMEM is released.
@@ -47,18 +50,20 @@ namespace {
 
 constexpr int KT = 128;                             // keys of a tile
 constexpr int M = 128;                              // query rows of an item
-constexpr int LWARPS = 4;                           // loader warps (more leave the softmax fewer than 128 registers)
-constexpr int W_LOAD = 8, W_MMA = W_LOAD + LWARPS;
+constexpr int W_LOAD = 8, LWARPS = 4, W_MMA = 12, W_TMA = 13;
 constexpr int LOADERS = 32 * LWARPS;
-constexpr int THREADS = 32 * (W_MMA + 1);
+constexpr int THREADS = 512;                        // warps 14 and 15 only make up the last warpgroup
+constexpr int REGS_SOFT = 168, REGS_REST = 88;
+static_assert(256 * (REGS_SOFT + REGS_REST) <= 65536, "register split");
 constexpr int RT = LOADERS / 8, RJ = KT / RT;       // cp.async: rows of a pass, passes of a tile
 constexpr uint32_t SLOT = 16384;
-constexpr int NS = 10;                              // slots of the ring
-constexpr uint32_t OFF_RING = 65536;                // Q: up to 128 rows x 512 B
-constexpr uint32_t OFF_XCH = OFF_RING + NS * SLOT;  // softmax exchange [2][2][128] floats
+constexpr int NS = 5;                               // slots of the K ring and of the V ring
+constexpr uint32_t OFF_K = 65536;                   // Q: up to 128 rows x 512 B
+constexpr uint32_t OFF_V = OFF_K + NS * SLOT;
+constexpr uint32_t OFF_XCH = OFF_V + NS * SLOT;     // softmax exchange [2][2][128] floats
 constexpr uint32_t OFF_OK = OFF_XCH + 2048;         // rows that are there, of NOK tiles, 32 bytes each
-// tiles whose row bits are live: the loaders run at most 6 tiles ahead of S (D =
-// 64: the ring holds 5), S 2 ahead of the softmax
+// tiles whose row bits are live: K runs at most 6 tiles ahead of S (D = 64: the
+// ring holds 5), S 2 ahead of the softmax
 constexpr int NOK = 16;
 constexpr uint32_t OFF_BAR = OFF_OK + 32 * NOK;
 constexpr uint32_t SMEM = OFF_BAR + 320;
@@ -73,6 +78,30 @@ __device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t c16) {
   return row * 128u + ((c16 ^ (row & 7u)) << 4);
 }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// mbar_wait with the thread suspended for up to 10 us at a time instead of
+// polling: sixteen warps that poll slow the others' shared-memory and
+// special-function instructions.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+        : "memory");
+    if (ok) return true;
+    if (it == 0) t0 = globaltimer();
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > QSA_WAIT_TIMEOUT_NS) {
+      *abort_flag = 1;
+      report_error(err, QSA_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+  }
+}
 // The barrier's phase waits for this thread's copies so far, beside its counted
 // arrivals (this form adds the arrival that it makes to the pending count).
 __device__ __forceinline__ void cp_async_hold(uint64_t* bar) {
@@ -86,20 +115,56 @@ __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* m,
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(dim), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
       : "memory");
 }
-// MN-major operand descriptor (128-byte swizzle): lbo = distance between
-// 64-element atoms along N, sbo = distance between 8-row groups along K.
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
-         (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
+// Operand descriptors, 128-byte swizzle, as constant fields and a start address:
+// K-major (rows of 64 elements, 8-row groups 1024 bytes apart) and MN-major (lbo
+// bytes between 64-element atoms along N, 1024 between 8-row groups along K).
+constexpr uint64_t DESC_K = (uint64_t)1u << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
+__host__ __device__ constexpr uint64_t desc_mn(uint32_t lbo) {
+  return (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
 }
-// O[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ uint64_t desc_at(uint64_t fields, uint32_t addr) { return fields | (addr >> 4); }
+// The MMA warp stays converged and one elected lane issues (always the same one):
+// descriptors and addresses then live in uniform registers.  Inside a one-lane
+// branch each MMA first moves them there, which took longer than the MMA.
+// D[tmem] (+)= A[smem] * B[smem]^T
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                         uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -140,10 +205,10 @@ __host__ __device__ inline Scratch scratch_of(void* p) {
 }
 
 struct Args {
-  CUtensorMap tk, tv;       // TMA: boxes of `box` rows x 64 dims
+  CUtensorMap tk;           // K pages, boxes of `box` rows x 64 dims
   PagedAttnArgs a;
   Grid grid;
-  int box;                  // 16 or 32, or 1: no TMA
+  int box;                  // 16, 32 or 64, or 1: no TMA
 };
 
 // Item w.  Sequence b owns the tile slots from cu[b] per / 128 + b on (at least
@@ -207,9 +272,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   const PagedAttnArgs& a = x.a;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-  uint64_t* full = bars;                            // [NS]
-  uint64_t* empty = full + NS;                      // [NS]
-  uint64_t* q_full = empty + NS;
+  uint64_t* k_full = bars;                          // [NS]
+  uint64_t* k_empty = k_full + NS;                  // [NS]
+  uint64_t* v_full = k_empty + NS;                  // [NS]
+  uint64_t* v_empty = v_full + NS;                  // [NS]
+  uint64_t* q_full = v_empty + NS;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_empty + 1;                   // [2]
   uint64_t* p_full = s_full + 2;                    // [2]
@@ -219,14 +286,19 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   uint64_t* mma_done = xbar + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile uint64_t* rows_ok = reinterpret_cast<volatile uint64_t*>(smem + OFF_OK);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the shuffle tells the compiler that a warp has one role
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (tid == 0) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
     return;
   }
   if (tid == 0) {
-    for (int s = 0; s < NS; ++s) { mbar_init(&full[s], LWARPS); mbar_init(&empty[s], 1); }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&k_full[s], TMA ? 1 : LWARPS);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], LWARPS);
+      mbar_init(&v_empty[s], 1);
+    }
     mbar_init(q_full, LWARPS);
     mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8); mbar_init(&pv_done[i], 1); }
@@ -245,291 +317,278 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   const int64_t n_items = x.grid.n_slots * a.hk * x.grid.n_split;
   const int per = a.hq / a.hk;
 
+  if (warp >= W_LOAD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
   if (warp >= W_LOAD && warp < W_MMA) {
-    // ---------------------------------------------------------------- loaders
-    const int lt = tid - 32 * W_LOAD, c = lt & 7, rt = lt >> 3;   // cp.async: 16-byte chunk, row of a pass
+    // ------------------------------------------- Q and V (and K without TMA)
+    const int lt = tid - 32 * W_LOAD, c = lt & 7, rt = lt >> 3;   // 16-byte chunk, row of a pass
     const int lw = warp - W_LOAD;
-    int slot = 0;
-    uint32_t eph = 1, items_done = 0, count = 0;   // tiles so far
-    uint32_t landing = 0;                          // slots with a TMA copy that the MMA may not have seen
+    int kslot = 0, vslot = 0;
+    uint32_t keph = 1, veph = 1, items_done = 0, count = 0;       // count: K tiles so far
     bool ok = true;
-    // one arrival per warp, after its lanes' copies are on their way; bytes: what
-    // the warp fetches by TMA
-    auto arrive = [&](uint64_t* bar, uint32_t bytes) {
+    // after the copies of this thread: the slot is full once every warp's have landed
+    auto done = [&](uint64_t* bar) {
+      cp_async_hold(bar);
       __syncwarp();
-      if (lane == 0) {
-        if (bytes) mbar_arrive_expect_tx(bar, bytes);
-        else mbar_arrive(bar);
-      }
+      if (lane == 0) mbar_arrive(bar);
     };
-    auto advance = [&]() { if (++slot == NS) { slot = 0; eph ^= 1; } };
     for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
       const Item it(x, w);
       if (it.n_tiles <= 0) continue;
       const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
       const int64_t head = (int64_t)it.g * a.kv.head_stride + 8 * c;
       auto key_of = [&](int v) { return v < it.ns ? v : it.lo + (v - it.ns); };
-      auto needed = [&](int key) { return key < it.end && (key >= it.first || key < a.sinks); };
-      // ---- by boxes (TMA): lane i of each warp knows box i of a tile
-      const int box = x.box, nb = KT / box, bs = box == 32 ? 5 : 4;   // box = 1 << bs
-      struct Box { int id, row; bool good, clean; };  // page, first row in it; there at all; every row needed
-      auto find_box = [&](int tile) -> Box {
-        const int key = key_of(tile * KT + (lane & (nb - 1)) * box);
-        // some row of the box is needed: its last row, or the first of those left by the sinks
-        const bool any = key < it.end && (key + box > it.first || key < a.sinks);
-        Box r;
-        r.id = any ? __ldg(table + page_of(a.kv, (uint32_t)key)) : -1;
-        r.good = (uint32_t)r.id < (uint32_t)a.kv.n_pages;
-        if (any && !r.good) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
-        r.row = key - (int)(page_of(a.kv, (uint32_t)key) * (uint32_t)a.kv.page_size);
-        r.clean = r.good && key + box <= it.end && (key >= it.first || key + box <= a.sinks);
-        return r;
-      };
-      // ---- row by row: this thread's rows rt + RT j of a tile, the page ids
-      // loaded a tile ahead, all at once
-      int32_t ids[RJ];
+      // Page ids of this thread's rows rt + RT j of a tile: loaded a tile ahead,
+      // all at once.
+      int ids[RJ];
       auto load_ids = [&](int tile) {
 #pragma unroll
         for (int j = 0; j < RJ; ++j) {
-          const int key = key_of(min(tile * KT + RT * j + rt, it.n_vis - 1));
-          ids[j] = __ldg(table + page_of(a.kv, (uint32_t)max(key, 0)));
+          const int key = key_of(max(min(tile * KT + RT * j + rt, it.n_vis - 1), 0));
+          ids[j] = __ldg(table + page_of(a.kv, (uint32_t)min(key, a.kv.capacity - 1)));
         }
       };
-      auto row_off = [&](int key, int id) -> int64_t {
-        const int in_page = key - (int)(page_of(a.kv, (uint32_t)key) * (uint32_t)a.kv.page_size);
-        return (int64_t)id * a.kv.page_stride + (int64_t)in_page * a.kv.token_stride + head;
-      };
-      Box bk{}, bv{}, bn{};                          // boxes of the K tile, the V tile, the next K tile
-      int64_t off_k[TMA ? 1 : RJ], off_v[TMA ? 1 : RJ];
-      if (TMA) bn = find_box(it.tile0);
-      else load_ids(it.tile0);
-      auto begin_tile = [&](int tile) {
-        const uint32_t at = (count % NOK) * 32;
-        if constexpr (TMA) {
-          bk = bn;
-          const uint32_t good = __ballot_sync(0xffffffffu, bk.good);
-          if (lw == 0) reinterpret_cast<volatile uint8_t*>(rows_ok)[at + lane] = (good >> ((4 * lane) >> bs)) & 1 ? 15 : 0;
-          bn = find_box(tile + 1);
-        } else {
+      // A tile's rows: offset of this thread's chunk, and whether the row is there
+      // (some query sees it and its page is one).
+      struct Rows { int64_t off[RJ]; uint32_t ok; };
+      auto find_rows = [&](int tile, Rows& d) {
+        d.ok = 0;
+        uint32_t bad = 0;
 #pragma unroll
-          for (int j = 0; j < RJ; ++j) {
-            const int v = tile * KT + RT * j + rt;
-            const bool there = v < it.n_vis, good = there && (uint32_t)ids[j] < (uint32_t)a.kv.n_pages;
-            if (there && !good) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
-            off_k[j] = good ? row_off(key_of(v), ids[j]) : -1;
-            // the warp's four rows of the pass: one byte of their bits
-            const uint32_t bits = __ballot_sync(0xffffffffu, good && c == 0);
-            if (lane == 0) {
-              const uint32_t four = (bits & 1) | (bits >> 7 & 2) | (bits >> 14 & 4) | (bits >> 21 & 8);
-              reinterpret_cast<volatile uint8_t*>(rows_ok)[at + j * LWARPS + lw] = (uint8_t)four;
-            }
+        for (int j = 0; j < RJ; ++j) {
+          const int v = tile * KT + RT * j + rt, key = key_of(v);
+          const bool needed = v < it.n_vis && (key >= it.first || key < a.sinks);
+          const bool good = needed && (uint32_t)ids[j] < (uint32_t)a.kv.n_pages;
+          const int in_page = key - (int)(page_of(a.kv, (uint32_t)key) * (uint32_t)a.kv.page_size);
+          d.off[j] = good ? (int64_t)ids[j] * a.kv.page_stride + (int64_t)in_page * a.kv.token_stride + head : 0;
+          d.ok |= (uint32_t)good << j;
+          bad |= (uint32_t)(needed && !good);
+        }
+        if (bad) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
+      };
+      const uint32_t lane_dst = swz128(rt, c);         // rows of a pass are 16 apart: the same swizzle in each
+      auto load_k = [&](const Rows& d) -> bool {
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) {
+          // the warp's four rows of the pass: one byte of their bits
+          const uint32_t bits = __ballot_sync(0xffffffffu, (d.ok >> j & 1) && c == 0);
+          if (lane == 0) {
+            const uint32_t four = (bits & 1) | (bits >> 7 & 2) | (bits >> 14 & 4) | (bits >> 21 & 8);
+            reinterpret_cast<volatile uint8_t*>(smem + OFF_OK)[(count % NOK) * 32 + j * LWARPS + lw] = (uint8_t)four;
           }
-          load_ids(tile + 1);
         }
         ++count;
-      };
-      auto load_k = [&]() -> bool {
         for (int ch = 0; ch < NCH; ++ch) {
-          if (!mbar_wait(&empty[slot], eph, abort_flag, a.err)) return false;
-          const uint32_t dst = smem_u32(smem + OFF_RING + slot * SLOT);
-          if constexpr (TMA) {
-            uint32_t bytes = 0;
-            if (lw == 0) {
-              const bool mine = lane < nb && bk.good;
-              bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box * 128;
-              if (bytes) landing |= 1u << slot;
-              arrive(&full[slot], bytes);
-              if (mine) tma_load_box(dst + lane * box * 128, &x.tk, 64 * ch, bk.row, it.g, bk.id, &full[slot]);
-            } else {
-              arrive(&full[slot], 0);
-            }
-          } else {
+          if (!bar_wait(&k_empty[kslot], keph, abort_flag, a.err)) return false;
+          const uint32_t dst = smem_u32(smem + OFF_K + kslot * SLOT) + lane_dst;
 #pragma unroll
-            for (int j = 0; j < RJ; ++j) {
-              const bool valid = off_k[j] >= 0;
-              cp_async16_zfill(dst + swz128(RT * j + rt, c), valid ? a.kv.k + off_k[j] + 64 * ch : a.kv.k, valid);
-            }
-            cp_async_hold(&full[slot]);
-            arrive(&full[slot], 0);
-          }
-          advance();
+          for (int j = 0; j < RJ; ++j)
+            cp_async16_zfill(dst + RT * j * 128, a.kv.k + d.off[j] + 64 * ch, d.ok >> j & 1);
+          done(&k_full[kslot]);
+          if (++kslot == NS) { kslot = 0; keph ^= 1; }
         }
         return true;
       };
-      auto load_v = [&](int tile) -> bool {
+      auto load_v = [&](const Rows& d) -> bool {
 #pragma unroll
         for (int s = 0; s < NCH; ++s) {
-          if (!mbar_wait(&empty[slot], eph, abort_flag, a.err)) return false;
-          const uint32_t dst = smem_u32(smem + OFF_RING + slot * SLOT);
-          if constexpr (TMA) {
-            const int b0 = s * KV >> bs, n = KV >> bs;   // the slot's boxes
-            const uint32_t clean = __ballot_sync(0xffffffffu, bv.clean) >> b0;
-            if ((~clean & ((1u << n) - 1)) == 0) {
-              const int i = lane / NCH, ch = lane % NCH;
-              const int id = __shfl_sync(0xffffffffu, bv.id, (b0 + i) & 31), row = __shfl_sync(0xffffffffu, bv.row, (b0 + i) & 31);
-              if (lw == 0) {
-                landing |= 1u << slot;
-                arrive(&full[slot], SLOT);
-                if (i < n)                            // n NCH is 4 or 8
-                  tma_load_box(dst + ch * (KV * 128) + i * box * 128, &x.tv, 64 * ch, row, it.g, id, &full[slot]);
-              } else {
-                arrive(&full[slot], 0);
-              }
-              advance();
-              continue;
-            }
+          if (!bar_wait(&v_empty[vslot], veph, abort_flag, a.err)) return false;
+          const uint32_t dst = smem_u32(smem + OFF_V + vslot * SLOT) + lane_dst;
 #pragma unroll
-            for (int j = 0; j < KV / RT; ++j) {
-              const int r = s * KV + RT * j + rt, from = r >> bs;
-              const int key = key_of(tile * KT + r);
-              const int id = __shfl_sync(0xffffffffu, bv.id, from);
-              const bool valid = needed(key) && (uint32_t)id < (uint32_t)a.kv.n_pages;
-              const int64_t o = valid ? row_off(key, id) : 0;
+          for (int j = 0; j < KV / RT; ++j) {
+            const uint16_t* src = a.kv.v + d.off[s * (KV / RT) + j];
+            const bool there = d.ok >> (s * (KV / RT) + j) & 1;
 #pragma unroll
-              for (int ch = 0; ch < NCH; ++ch)
-                cp_async16_zfill(dst + ch * (KV * 128) + swz128(RT * j + rt, c), valid ? a.kv.v + o + 64 * ch : a.kv.v,
-                                 valid);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < KV / RT; ++j) {
-              const int64_t o = off_v[s * (KV / RT) + j];
-              const bool valid = o >= 0;
-#pragma unroll
-              for (int ch = 0; ch < NCH; ++ch)
-                cp_async16_zfill(dst + ch * (KV * 128) + swz128(RT * j + rt, c), valid ? a.kv.v + o + 64 * ch : a.kv.v,
-                                 valid);
-            }
+            for (int ch = 0; ch < NCH; ++ch) cp_async16_zfill(dst + ch * (KV * 128) + RT * j * 128, src + 64 * ch, there);
           }
-          cp_async_hold(&full[slot]);
-          arrive(&full[slot], 0);
-          advance();
+          done(&v_full[vslot]);
+          if (++vslot == NS) { vslot = 0; veph ^= 1; }
         }
         return true;
       };
-      for (int i = 0; ok && i <= it.n_tiles; ++i) {
-        if (i < it.n_tiles) {
-          begin_tile(it.tile0 + i);
-          if (!load_k()) { ok = false; break; }
+      auto load_q = [&]() -> bool {
+        // once the previous item's last S has read its own
+        if (items_done > 0 && !bar_wait(q_empty, (items_done - 1) & 1, abort_flag, a.err)) return false;
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) {
+          const int r = RT * j + rt;
+          const bool valid = r < it.rows;
+          const int64_t f = it.row0 + (valid ? r : 0);
+          const uint16_t* src = a.q + ((it.t0 + f / per) * a.hq + it.g * per + f % per) * D + 8 * c;
+#pragma unroll
+          for (int ch = 0; ch < NCH; ++ch)
+            cp_async16_zfill(smem_u32(smem + ch * SLOT) + swz128(r, c), valid ? src + 64 * ch : a.q, valid);
         }
-        if (i == 0) {
-          // queries, once the previous item's last S has read its own
-          if (items_done > 0 && !mbar_wait(q_empty, (items_done - 1) & 1, abort_flag, a.err)) { ok = false; break; }
-#pragma unroll
-          for (int j = 0; j < RJ; ++j) {
-            const int r = RT * j + rt;
-            const bool valid = r < it.rows;
-            const int64_t f = it.row0 + (valid ? r : 0);
-            const uint16_t* src = a.q + ((it.t0 + f / per) * a.hq + it.g * per + f % per) * D + 8 * c;
-#pragma unroll
-            for (int ch = 0; ch < NCH; ++ch)
-              cp_async16_zfill(smem_u32(smem + ch * SLOT) + swz128(r, c), valid ? src + 64 * ch : a.q, valid);
+        done(q_full);
+        return true;
+      };
+      load_ids(it.tile0);
+      if constexpr (TMA) {
+        ok = load_q();
+        for (int i = 0; ok && i < it.n_tiles; ++i) {
+          Rows d;
+          find_rows(it.tile0 + i, d);
+          load_ids(it.tile0 + i + 1);
+          ok = load_v(d);
+        }
+      } else {
+        Rows d{};
+        for (int i = 0; ok && i <= it.n_tiles; ++i) {
+          const Rows before = d;
+          if (i < it.n_tiles) {
+            find_rows(it.tile0 + i, d);
+            load_ids(it.tile0 + i + 1);
+            ok = load_k(d);
           }
-          cp_async_hold(q_full);
-          arrive(q_full, 0);
-        } else if (!load_v(it.tile0 + i - 1)) {
-          ok = false;
-          break;
-        }
-        if constexpr (TMA) {
-          bv = bk;
-        } else {
-#pragma unroll
-          for (int j = 0; j < RJ; ++j) off_v[j] = off_k[j];
+          if (ok) ok = i == 0 ? load_q() : load_v(before);
         }
       }
       ++items_done;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (TMA && warp == W_TMA) {
+    // ---------------------------------------------------------------------- K
+    int slot = 0;
+    uint32_t eph = 1, count = 0, landing = 0;      // landing: slots that a copy went to
+    bool ok = true;
+    const int box = x.box, nb = KT / box;
+    for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
+      const Item it(x, w);
+      if (it.n_tiles <= 0) continue;
+      const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
+      // lane i has box i of a tile (lanes past the last repeat): its page, or -1
+      // where no row of it is needed or the page is none, and its first row there
+      auto find = [&](int tile, int& id, int& row) {
+        const int v = tile * KT + (lane & (nb - 1)) * box, key = v < it.ns ? v : it.lo + (v - it.ns);
+        const uint32_t pg = page_of(a.kv, (uint32_t)key);
+        const bool any = v < it.n_vis && (key + box > it.first || key < a.sinks);
+        id = any ? __ldg(table + pg) : -1;
+        if (any && (uint32_t)id >= (uint32_t)a.kv.n_pages) {
+          report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
+          id = -1;
+        }
+        row = key - (int)(pg * (uint32_t)a.kv.page_size);
+      };
+      int id, row, id_n, row_n;
+      find(it.tile0, id_n, row_n);
+      for (int i = 0; ok && i < it.n_tiles; ++i) {
+        id = id_n;
+        row = row_n;
+        const uint32_t good = __ballot_sync(0xffffffffu, id >= 0);
+        reinterpret_cast<volatile uint8_t*>(smem + OFF_OK)[(count % NOK) * 32 + lane] = good >> (4 * lane / box) & 1 ? 15 : 0;
+        ++count;
+        if (i + 1 < it.n_tiles) find(it.tile0 + i + 1, id_n, row_n);
+        const bool mine = lane < nb && id >= 0;
+        const uint32_t bytes = (uint32_t)__popc(good & ((1u << nb) - 1)) * box * 128;
+        for (int ch = 0; ch < NCH; ++ch) {
+          if (!__all_sync(0xffffffffu, bar_wait(&k_empty[slot], eph, abort_flag, a.err))) { ok = false; break; }
+          if (lane == 0) {
+            if (bytes) mbar_arrive_expect_tx(&k_full[slot], bytes);
+            else mbar_arrive(&k_full[slot]);
+          }
+          __syncwarp();
+          if (bytes) landing |= 1u << slot;
+          if (mine)
+            tma_load_box(smem_u32(smem + OFF_K + slot * SLOT) + lane * box * 128, &x.tk, 64 * ch, row, it.g, id, &k_full[slot]);
+          if (++slot == NS) { slot = 0; eph ^= 1; }
+        }
+      }
+    }
     // After an abort no TMA copy may still be writing when the CTA exits: wait
-    // for the last phase of every slot that one went to (without an abort the
-    // MMA has waited for all of them, and these return at once).
-    if (TMA && lw == 0 && lane == 0)
+    // for the last phase of every slot that one went to (without an abort the MMA
+    // waits for all of them).
+    if (lane == 0)
       for (int s = 0; s < NS; ++s)
-        if (landing >> s & 1) mbar_wait_drain(&full[s], (s < slot ? eph : eph ^ 1) ^ 1, a.err);
+        if (landing >> s & 1) mbar_wait_drain(&k_full[s], (s < slot ? eph : eph ^ 1) ^ 1, a.err);
   } else if (warp == W_MMA) {
     // -------------------------------------------------------------------- MMA
-    if (lane == 0) {
-      int slot = 0;
-      uint32_t fph = 0, items_done = 0, s_count = 0, p_count = 0;
-      bool ok = true;
-      const uint32_t q_base = smem_u32(smem);
-      auto take = [&](uint32_t& base) -> bool {     // the next full slot
-        if (!mbar_wait(&full[slot], fph, abort_flag, a.err)) return false;
-        fence_async_proxy();                        // written by cp.async, read by the MMA
-        tc_fence_after();
-        base = smem_u32(smem + OFF_RING + slot * SLOT);
-        return true;
-      };
-      auto done = [&]() {
-        tc_commit(&empty[slot]);
-        if (++slot == NS) { slot = 0; fph ^= 1; }
-      };
-      for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
-        const Item it(x, w);
-        if (it.n_tiles <= 0) continue;
-        if (!mbar_wait(q_full, items_done & 1, abort_flag, a.err)) { ok = false; break; }
-        for (int i = 0; ok && i <= it.n_tiles; ++i) {
-          if (i < it.n_tiles) {
-            // S(i) overwrites the buffer of P(i - 2), which P V(i - 2), issued
-            // before it by this thread, has read by then
-            const uint32_t d = tmem + TM_S + 128 * (s_count & 1);
-            for (int ch = 0; ch < NCH; ++ch) {
-              uint32_t kb;
-              if (!take(kb)) { ok = false; break; }
+    int kslot = 0, vslot = 0;
+    uint32_t kph = 0, vph = 0, items_done = 0, s_count = 0, p_count = 0;
+    bool ok = true;
+    const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
+    };
+    for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
+      const Item it(x, w);
+      const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
+      if (n_tiles <= 0) continue;
+      if (!wait(q_full, items_done & 1)) { ok = false; break; }
+      fence_async_proxy();                          // Q: written by cp.async, read by the MMA
+      for (int i = 0; ok && i <= n_tiles; ++i) {
+        if (i < n_tiles) {
+          // S(i) overwrites the buffer of P(i - 2), which P V(i - 2), issued
+          // before it by the same lane, has read by then
+          const uint32_t d = tm + TM_S + 128 * (s_count & 1);
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                umma_bf16(d, umma_desc_k_sw128(q_base + ch * SLOT + 32 * ks), umma_desc_k_sw128(kb + 32 * ks), IDESC,
-                          ch > 0 || ks > 0 ? 1u : 0u);
-              done();
-            }
-            if (!ok) break;
-            tc_commit(&s_full[s_count & 1]);
-            if (i == it.n_tiles - 1) tc_commit(q_empty);
-            ++s_count;
-          }
-          if (i > 0) {
-            const uint32_t p = tmem + TM_S + 128 * (p_count & 1);
-            if (!mbar_wait(&p_full[p_count & 1], (p_count >> 1) & 1, abort_flag, a.err)) { ok = false; break; }
-            if (i == 1 && items_done > 0 && !mbar_wait(o_empty, (items_done - 1) & 1, abort_flag, a.err)) {
-              ok = false;
-              break;
-            }
-            for (int s = 0; s < NCH; ++s) {
-              uint32_t vb;
-              if (!take(vb)) { ok = false; break; }
+          for (int ch = 0; ch < NCH; ++ch) {
+            if (!wait(&k_full[kslot], kph)) { ok = false; break; }
+            if (!TMA) fence_async_proxy();
+            tc_fence_after();
+            const uint32_t kb = base + OFF_K + kslot * SLOT;
 #pragma unroll
-              for (int ks = 0; ks < KV / 16; ++ks)
-                umma_ts(tmem + TM_O, p + 8 * (s * (KV / 16) + ks), desc_mn_sw128(vb + 2048 * ks, KV * 128, 1024),
-                        IDESC_PV, i > 1 || s > 0 || ks > 0 ? 1u : 0u);
-              done();
-            }
-            if (!ok) break;
-            tc_commit(&pv_done[p_count & 1]);
-            ++p_count;
+            for (int ks = 0; ks < 4; ++ks)
+              umma_ss(d, desc_at(DESC_K, base + ch * SLOT + 32 * ks), desc_at(DESC_K, kb + 32 * ks), IDESC,
+                      ch > 0 || ks > 0 ? 1u : 0u);
+            umma_commit(&k_empty[kslot]);
+            if (++kslot == NS) { kslot = 0; kph ^= 1; }
           }
+          if (!ok) break;
+          umma_commit(&s_full[s_count & 1]);
+          if (i == n_tiles - 1) umma_commit(q_empty);
+          ++s_count;
         }
-        ++items_done;
+        if (i > 0) {
+          const uint32_t p = tm + TM_S + 128 * (p_count & 1);
+          // V is long there when P comes: one fence for all of a tile's slots
+          int vs = vslot;
+          uint32_t vp = vph;
+#pragma unroll
+          for (int s = 0; s < NCH; ++s) {
+            if (!wait(&v_full[vs], vp)) ok = false;
+            if (++vs == NS) { vs = 0; vp ^= 1; }
+          }
+          fence_async_proxy();                      // written by cp.async, read by the MMA
+          if (!ok || !wait(&p_full[p_count & 1], (p_count >> 1) & 1)) { ok = false; break; }
+          if (i == 1 && items_done > 0 && !wait(o_empty, (items_done - 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < NCH; ++s) {
+            const uint32_t vb = base + OFF_V + vslot * SLOT;
+#pragma unroll
+            for (int ks = 0; ks < KV / 16; ++ks)
+              umma_ts(tm + TM_O, p + 8 * (s * (KV / 16) + ks), desc_at(desc_mn(KV * 128), vb + 2048 * ks), IDESC_PV,
+                      i > 1 || s > 0 || ks > 0 ? 1u : 0u);
+            umma_commit(&v_empty[vslot]);
+            if (++vslot == NS) { vslot = 0; vph ^= 1; }
+          }
+          umma_commit(&pv_done[p_count & 1]);
+          ++p_count;
+        }
       }
-      // every MMA this thread issued has retired before TMEM is released (also
-      // after an abort: a wait that ignores the flag)
-      tc_commit(mma_done);
-      mbar_wait_drain(mma_done, 0, a.err);
+      ++items_done;
     }
+    // every MMA of this warp has retired before TMEM is released (also after an
+    // abort: a wait that ignores the flag)
+    umma_commit(mma_done);
+    mbar_wait_drain(mma_done, 0, a.err);
   } else if (warp < W_LOAD) {
     // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
     const int quad = warp & 3, half = warp >> 2;    // rows 32 quad .., scores 64 half ..
     const int r = 32 * quad + lane;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     float* xch = reinterpret_cast<float*>(smem + OFF_XCH);   // [2][2 halves][128 rows]
     uint32_t xc = 0, count = 0, items_done = 0;
     bool ok = true;
-    auto exchange = [&](float mine, float& other) -> bool {
-      const uint32_t s = (xc & 1) * 2;
-      xch[(s + half) * M + r] = mine;
+    // hand a value to the row's other thread, and take its own
+    auto give = [&](float mine) {
+      xch[((xc & 1) * 2 + half) * M + r] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(&xbar[quad]);
-      const bool okx = __all_sync(0xffffffffu, mbar_wait(&xbar[quad], xc & 1, abort_flag, a.err));
+    };
+    auto take = [&](float& other) -> bool {
+      const uint32_t s = (xc & 1) * 2;
+      const bool okx = __all_sync(0xffffffffu, bar_wait(&xbar[quad], xc & 1, abort_flag, a.err));
       other = xch[(s + (half ^ 1)) * M + r];
       ++xc;
       return okx;
@@ -560,7 +619,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       float m = -FLT_MAX, l = 0.f;
       for (int i = 0; i < n_tiles; ++i, ++count, v0 += KT) {
         const uint32_t buf = count & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], (count >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, bar_wait(&s_full[buf], (count >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
         tc_fence_after();
         const uint32_t s_addr = tmem + lanes + TM_S + 128 * buf;
         float s0[32], s1[32];
@@ -584,6 +643,28 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
             if (!okc) s1[e] = -INFINITY;
           }
         }
+        // p = 2^(s scale - m) under the maximum so far, while the tile's own is
+        // found and handed over; the sum takes the fp32 values, the products p
+        // rounded to 16 bits
+        float sum;
+        uint32_t pk[32];
+        auto exps = [&]() {
+          const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-m, -m);
+          uint64_t t = pk2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float x0, x1;
+            upk2(fma2(e < 16 ? pk2(s0[2 * (e & 15)], s0[2 * (e & 15) + 1]) : pk2(s1[2 * (e & 15)], s1[2 * (e & 15) + 1]),
+                      sc2, nm2), x0, x1);
+            x0 = exp2_approx(x0);
+            x1 = exp2_approx(x1);
+            t = add2(t, pk2(x0, x1));
+            pk[e] = X::pack(x0, x1);
+          }
+          float t0, t1;
+          upk2(t, t0, t1);
+          sum = t0 + t1;
+        };
         float mt = max3f(s0[0], s1[0], s0[1]), mu = max3f(s1[1], s0[2], s1[2]);
 #pragma unroll
         for (int e = 3; e + 1 < 32; e += 2) {
@@ -592,11 +673,15 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
         }
         mt = max3f(mt, s0[31], s1[31]);
         mt = fmaxf(fmaxf(mt, mu) * a.scale_log2, -FLT_MAX);   // a tile without a key leaves the maximum as it is
+        give(mt);
+        if (i > 0) exps();
+        // from here on the other half has read its scores, which P overwrites
         float other;
-        if (!exchange(mt, other)) { ok = false; break; }
+        if (!take(other)) { ok = false; break; }
         mt = fmaxf(mt, other);
         const bool raise = mt > m + RAISE;
-        if (__any_sync(0xffffffffu, raise)) {
+        const bool any = __any_sync(0xffffffffu, raise);
+        if (any) {
           const float nm = raise ? mt : m;
           const float f = exp2_approx(m - nm);
           l *= f;
@@ -605,7 +690,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
             // O holds the tiles up to i - 1 once their P V is done; this tile's
             // waits for this warp
             const uint32_t g = count - 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[g & 1], (g >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, bar_wait(&pv_done[g & 1], (g >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
             for (int cc = 0; cc < D / 32; ++cc) {
@@ -616,30 +701,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
               tmem_st16(ad, o);
             }
-            tmem_st_wait();
           }
         }
-        // p = 2^(s scale - m); the sum takes the fp32 values, the products p rounded to 16 bits
-        const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-m, -m);
-        uint64_t sum = pk2(0.f, 0.f);
-        uint32_t pk[16];
-        auto exps = [&](const float (&sv)[32], uint32_t addr) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float x0, x1;
-            upk2(fma2(pk2(sv[2 * e], sv[2 * e + 1]), sc2, nm2), x0, x1);
-            x0 = exp2_approx(x0);
-            x1 = exp2_approx(x1);
-            sum = add2(sum, pk2(x0, x1));
-            pk[e] = X::pack(x0, x1);
-          }
-          tmem_st16(addr, pk);
-        };
-        exps(s0, s_addr + 32 * half);
-        exps(s1, s_addr + 32 * half + 16);
-        float l0, l1;
-        upk2(sum, l0, l1);
-        l += l0 + l1;
+        if (any || i == 0) exps();
+        l += sum;
+        tmem_st32(s_addr + 32 * half, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -648,10 +714,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       if (!ok) break;
       // ---- O / l
       const uint32_t g = count - 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[g & 1], (g >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, bar_wait(&pv_done[g & 1], (g >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
       tc_fence_after();
       float l_other;
-      if (!exchange(l, l_other)) { ok = false; break; }
+      give(l);
+      if (!take(l_other)) { ok = false; break; }
       const float lr = l + l_other;
       const float inv = lr == 0.f ? 0.f : 1.f / lr;   // no key at all: zero
       const float lse2 = lr == 0.f ? -INFINITY : m + log2f(lr);
@@ -759,11 +826,9 @@ cudaError_t launch_attn(const Args& x, int grid, cudaStream_t s) {
 }
 
 template <class E, int D>
-cudaError_t launch_d(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int num_sms, cudaStream_t s,
-                     bool join) {
+cudaError_t launch_d(const PagedAttnArgs& a, const CUtensorMap& tk, int num_sms, cudaStream_t s, bool join) {
   Args x;
   x.tk = tk;
-  x.tv = tv;
   x.a = a;
   x.grid = grid_of(a, num_sms);
   x.box = paged_prefill_box(a.kv.page_size);
@@ -790,19 +855,20 @@ size_t paged_prefill_scratch(int head_dim) { return (size_t)MAX_PIECES * M * (he
 
 bool paged_prefill_splits(const PagedAttnArgs& a, int num_sms) { return grid_of(a, num_sms).n_split > 1; }
 
-int paged_prefill_box(int page_size) { return page_size % 32 == 0 ? 32 : (page_size % 16 == 0 ? 16 : 1); }
+int paged_prefill_box(int page_size) {
+  return page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : page_size % 16 == 0 ? 16 : 1;
+}
 
-cudaError_t launch_paged_prefill(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
-                                 int dtype, int num_sms, cudaStream_t s, bool join) {
+cudaError_t launch_paged_prefill(const PagedAttnArgs& a, const CUtensorMap& tk, int head_dim, int dtype, int num_sms, cudaStream_t s, bool join) {
   if (a.B <= 0 || a.T <= 0) return cudaSuccess;
   const bool bf = dtype == QSA_DTYPE_BF16;
   switch (head_dim) {
-    case 64: return bf ? launch_d<__nv_bfloat16, 64>(a, tk, tv, num_sms, s, join)
-                        : launch_d<__half, 64>(a, tk, tv, num_sms, s, join);
-    case 128: return bf ? launch_d<__nv_bfloat16, 128>(a, tk, tv, num_sms, s, join)
-                        : launch_d<__half, 128>(a, tk, tv, num_sms, s, join);
-    case 256: return bf ? launch_d<__nv_bfloat16, 256>(a, tk, tv, num_sms, s, join)
-                        : launch_d<__half, 256>(a, tk, tv, num_sms, s, join);
+    case 64: return bf ? launch_d<__nv_bfloat16, 64>(a, tk, num_sms, s, join)
+                        : launch_d<__half, 64>(a, tk, num_sms, s, join);
+    case 128: return bf ? launch_d<__nv_bfloat16, 128>(a, tk, num_sms, s, join)
+                        : launch_d<__half, 128>(a, tk, num_sms, s, join);
+    case 256: return bf ? launch_d<__nv_bfloat16, 256>(a, tk, num_sms, s, join)
+                        : launch_d<__half, 256>(a, tk, num_sms, s, join);
     default: return cudaErrorInvalidValue;
   }
 }
