@@ -12,12 +12,12 @@
 // keys that any row sees are numbered without the gap between sinks and window
 // and taken in tiles of 128.  Persistent CTAs (one per SM) walk the items, those
 // of the last tokens (the most keys) first.
-//   * warps 0-7 (softmax): two threads a query row (TMEM lane), each with half
-//     of a tile's 128 scores: mask, exp2 under the running maximum of the tiles
-//     before (base 2), P packed to 16 bits into the score buffer.  Meanwhile the
-//     halves swap their tile maxima; only a tile that exceeds the running one by
-//     more than 8 raises it, rescales O and is taken again.  At the end O / l and
-//     the log-sum-exp.
+//   * warps 0-7 (softmax): two warpgroups that take the tiles in turn, a thread a
+//     query row (TMEM lane): mask, tile maximum, the running maximum from the
+//     other group (raised only when a tile exceeds it by more than 8, so the
+//     rescale of O is rare), handed back at once, then exp2 in base 2 and P
+//     packed to 16 bits into the score buffer.  So one group's exponentials run
+//     beside the other's loads and maxima.  At the end O / l and the log-sum-exp.
 //   * warp 13 (K): slots of 128 keys x 64 dims by TMA, a box of 16 to 64 rows of
 //     a page at a time (the numbering of the keys is rounded so that no box
 //     crosses a page).  K rows that nobody sees need no care: their scores are
@@ -28,9 +28,8 @@
 //     too.  K by one engine and V by the other because neither feeds the tensor
 //     cores alone: a TMA box takes 52 + 3.2 cycles a row of 128 bytes (at most 40
 //     bytes a cycle), four warps of cp.async bring 32.
-//   * warp 12 (one thread): S(i + 1) = Q K^T (M = 128, N = 128) is issued before
-//     O += P V (N = D) of tile i, so the tensor cores work on one while the
-//     softmax makes the other's operand.
+//   * warp 12: S(i) = Q K^T (M = 128, N = 128); warp 14: O += P V (N = D).  Two
+//     issuers, so a ready P V never waits behind the next S.
 // Registers: 168 a softmax thread, 88 the others (setmaxnreg).
 // Every mbarrier wait is bounded (timeout -> error word, clean exit): on an abort
 // every role leaves its loop, the loaders wait for their own copies and the MMA
@@ -50,9 +49,9 @@ namespace {
 
 constexpr int KT = 128;                             // keys of a tile
 constexpr int M = 128;                              // query rows of an item
-constexpr int W_LOAD = 8, LWARPS = 4, W_MMA = 12, W_TMA = 13;
+constexpr int W_LOAD = 8, LWARPS = 4, W_MMA = 12, W_TMA = 13, W_PV = 14;
 constexpr int LOADERS = 32 * LWARPS;
-constexpr int THREADS = 512;                        // warps 14 and 15 only make up the last warpgroup
+constexpr int THREADS = 512;                        // warp 15 only makes up the last warpgroup
 constexpr int REGS_SOFT = 168, REGS_REST = 88;
 static_assert(256 * (REGS_SOFT + REGS_REST) <= 65536, "register split");
 constexpr int RT = LOADERS / 8, RJ = KT / RT;       // cp.async: rows of a pass, passes of a tile
@@ -60,13 +59,13 @@ constexpr uint32_t SLOT = 16384;
 constexpr int NS = 5;                               // slots of the K ring and of the V ring
 constexpr uint32_t OFF_K = 65536;                   // Q: up to 128 rows x 512 B
 constexpr uint32_t OFF_V = OFF_K + NS * SLOT;
-constexpr uint32_t OFF_XCH = OFF_V + NS * SLOT;     // softmax exchange [2][2][128] floats
+constexpr uint32_t OFF_XCH = OFF_V + NS * SLOT;     // running maxima [2][128], row sums [2][128]
 constexpr uint32_t OFF_OK = OFF_XCH + 2048;         // rows that are there, of NOK tiles, 32 bytes each
 // tiles whose row bits are live: K runs at most 6 tiles ahead of S (D = 64: the
 // ring holds 5), S 2 ahead of the softmax
 constexpr int NOK = 16;
 constexpr uint32_t OFF_BAR = OFF_OK + 32 * NOK;
-constexpr uint32_t SMEM = OFF_BAR + 320;
+constexpr uint32_t SMEM = OFF_BAR + 384;
 static_assert(SMEM <= 232448, "prefill smem");
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_S = 0, TM_O = 256;            // S / P buffers at 0 and 128
@@ -265,6 +264,7 @@ template <class E, int D, bool TMA>
 __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_constant__ Args x) {
   constexpr int NCH = D / 64;                       // 64-dim chunks: K (and V) slots of a tile
   constexpr int KV = KT / NCH;                      // keys of a V slot
+  constexpr int GR = NCH < 2 ? 1 : 2;               // slots to a "full" barrier
   constexpr uint32_t IDESC = umma_idesc_bf16_f32(M, KT) &
                              (std::is_same<E, __half>::value ? ~((1u << 7) | (1u << 10)) : ~0u);   // f16: 0
   constexpr uint32_t IDESC_PV = ((IDESC & ~(63u << 17)) | ((uint32_t)(D >> 3) << 17)) | (1u << 16);   // V MN-major
@@ -282,9 +282,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   uint64_t* p_full = s_full + 2;                    // [2]
   uint64_t* pv_done = p_full + 2;                   // [2]
   uint64_t* o_empty = pv_done + 2;
-  uint64_t* xbar = o_empty + 1;                     // [4]: 32 rows each
-  uint64_t* mma_done = xbar + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint64_t* hand = o_empty + 1;                     // [2][4]: the maximum after a tile, 32 rows each
+  uint64_t* xbar = hand + 8;                        // [4]: row sums, 32 rows each
+  uint64_t* mma_done = xbar + 4;                    // [2]: the S and the P V issuer
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // the shuffle tells the compiler that a warp has one role
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -294,17 +295,19 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   }
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&k_full[s], TMA ? 1 : LWARPS);
+      mbar_init(&k_full[s], TMA ? GR : LWARPS);
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], LWARPS);
       mbar_init(&v_empty[s], 1);
     }
     mbar_init(q_full, LWARPS);
     mbar_init(q_empty, 1);
-    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8); mbar_init(&pv_done[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1); }
+    for (int i = 0; i < 8; ++i) mbar_init(&hand[i], 1);
     mbar_init(o_empty, 8);
     for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 2);
-    mbar_init(mma_done, 1);
+    mbar_init(&mma_done[0], 1);
+    mbar_init(&mma_done[1], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -322,10 +325,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     // ------------------------------------------- Q and V (and K without TMA)
     const int lt = tid - 32 * W_LOAD, c = lt & 7, rt = lt >> 3;   // 16-byte chunk, row of a pass
     const int lw = warp - W_LOAD;
-    int kslot = 0, vslot = 0;
+    int kslot = 0, vslot = 0, kgrp = 0, vgrp = 0;                 // slot, and barrier of its group
     uint32_t keph = 1, veph = 1, items_done = 0, count = 0;       // count: K tiles so far
     bool ok = true;
-    // after the copies of this thread: the slot is full once every warp's have landed
+    // after the copies of this thread: full once every warp's have landed
     auto done = [&](uint64_t* bar) {
       cp_async_hold(bar);
       __syncwarp();
@@ -383,7 +386,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
 #pragma unroll
           for (int j = 0; j < RJ; ++j)
             cp_async16_zfill(dst + RT * j * 128, a.kv.k + d.off[j] + 64 * ch, d.ok >> j & 1);
-          done(&k_full[kslot]);
+          if (ch % GR == GR - 1) {
+            done(&k_full[kgrp]);
+            if (++kgrp == NS) kgrp = 0;
+          }
           if (++kslot == NS) { kslot = 0; keph ^= 1; }
         }
         return true;
@@ -400,7 +406,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
 #pragma unroll
             for (int ch = 0; ch < NCH; ++ch) cp_async16_zfill(dst + ch * (KV * 128) + RT * j * 128, src + 64 * ch, there);
           }
-          done(&v_full[vslot]);
+          if (s % GR == GR - 1) {
+            done(&v_full[vgrp]);
+            if (++vgrp == NS) vgrp = 0;
+          }
           if (++vslot == NS) { vslot = 0; veph ^= 1; }
         }
         return true;
@@ -447,8 +456,9 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (TMA && warp == W_TMA) {
     // ---------------------------------------------------------------------- K
-    int slot = 0;
-    uint32_t eph = 1, count = 0, landing = 0;      // landing: slots that a copy went to
+    int slot = 0, grp = 0;
+    uint32_t eph = 1, gph = 0, count = 0;          // gph: parity of a group's barrier
+    uint32_t landing = 0, open = 0;                // groups that copies went to; arrivals of an unfinished one
     bool ok = true;
     const int box = x.box, nb = KT / box;
     for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
@@ -482,27 +492,33 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
         for (int ch = 0; ch < NCH; ++ch) {
           if (!__all_sync(0xffffffffu, bar_wait(&k_empty[slot], eph, abort_flag, a.err))) { ok = false; break; }
           if (lane == 0) {
-            if (bytes) mbar_arrive_expect_tx(&k_full[slot], bytes);
-            else mbar_arrive(&k_full[slot]);
+            if (bytes) mbar_arrive_expect_tx(&k_full[grp], bytes);
+            else mbar_arrive(&k_full[grp]);
           }
           __syncwarp();
-          if (bytes) landing |= 1u << slot;
+          if (bytes) landing |= 1u << grp;
+          open = (ch + 1) % GR;
           if (mine)
-            tma_load_box(smem_u32(smem + OFF_K + slot * SLOT) + lane * box * 128, &x.tk, 64 * ch, row, it.g, id, &k_full[slot]);
+            tma_load_box(smem_u32(smem + OFF_K + slot * SLOT) + lane * box * 128, &x.tk, 64 * ch, row, it.g, id, &k_full[grp]);
           if (++slot == NS) { slot = 0; eph ^= 1; }
+          if (ch % GR == GR - 1) {
+            if (++grp == NS) { grp = 0; gph ^= 1; }
+          }
         }
       }
     }
     // After an abort no TMA copy may still be writing when the CTA exits: wait
-    // for the last phase of every slot that one went to (without an abort the MMA
-    // waits for all of them).
-    if (lane == 0)
-      for (int s = 0; s < NS; ++s)
-        if (landing >> s & 1) mbar_wait_drain(&k_full[s], (s < slot ? eph : eph ^ 1) ^ 1, a.err);
+    // for the last phase of every group that copies went to (without an abort the
+    // MMA waits for all of them).
+    if (lane == 0) {
+      if (open) mbar_arrive(&k_full[grp]);         // the group that an abort left half issued (GR = 2)
+      for (int g = 0; g < NS; ++g)
+        if (landing >> g & 1) mbar_wait_drain(&k_full[g], g < grp || (open && g == grp) ? gph : gph ^ 1, a.err);
+    }
   } else if (warp == W_MMA) {
-    // -------------------------------------------------------------------- MMA
-    int kslot = 0, vslot = 0;
-    uint32_t kph = 0, vph = 0, items_done = 0, s_count = 0, p_count = 0;
+    // ---------------------------------------------------------------------- S
+    int kslot = 0, kgrp = 0;
+    uint32_t kph = 0, items_done = 0, count = 0;
     bool ok = true;
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -514,84 +530,89 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       if (n_tiles <= 0) continue;
       if (!wait(q_full, items_done & 1)) { ok = false; break; }
       fence_async_proxy();                          // Q: written by cp.async, read by the MMA
-      for (int i = 0; ok && i <= n_tiles; ++i) {
-        if (i < n_tiles) {
-          // S(i) overwrites the buffer of P(i - 2), which P V(i - 2), issued
-          // before it by the same lane, has read by then
-          const uint32_t d = tm + TM_S + 128 * (s_count & 1);
+      for (int i = 0; i < n_tiles; ++i, ++count) {
+        // S overwrites the buffer of the P two tiles before: its P V is done.
+        // (That barrier's next phase needs this S, so its parity is exact.)
+        if (count >= 2 && !wait(&pv_done[count & 1], ((count >> 1) - 1) & 1)) { ok = false; break; }
+        const uint32_t d = tm + TM_S + 128 * (count & 1);
 #pragma unroll
-          for (int ch = 0; ch < NCH; ++ch) {
-            if (!wait(&k_full[kslot], kph)) { ok = false; break; }
+        for (int ch = 0; ch < NCH; ++ch) {
+          if (ch % GR == 0) {
+            if (!wait(&k_full[kgrp], kph)) { ok = false; break; }
+            if (++kgrp == NS) { kgrp = 0; kph ^= 1; }
             if (!TMA) fence_async_proxy();
             tc_fence_after();
-            const uint32_t kb = base + OFF_K + kslot * SLOT;
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_ss(d, desc_at(DESC_K, base + ch * SLOT + 32 * ks), desc_at(DESC_K, kb + 32 * ks), IDESC,
-                      ch > 0 || ks > 0 ? 1u : 0u);
-            umma_commit(&k_empty[kslot]);
-            if (++kslot == NS) { kslot = 0; kph ^= 1; }
           }
-          if (!ok) break;
-          umma_commit(&s_full[s_count & 1]);
-          if (i == n_tiles - 1) umma_commit(q_empty);
-          ++s_count;
+          const uint32_t kb = base + OFF_K + kslot * SLOT;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_ss(d, desc_at(DESC_K, base + ch * SLOT + 32 * ks), desc_at(DESC_K, kb + 32 * ks), IDESC,
+                    ch > 0 || ks > 0 ? 1u : 0u);
+          umma_commit(&k_empty[kslot]);
+          if (++kslot == NS) kslot = 0;
         }
-        if (i > 0) {
-          const uint32_t p = tm + TM_S + 128 * (p_count & 1);
-          // V is long there when P comes: one fence for all of a tile's slots
-          int vs = vslot;
-          uint32_t vp = vph;
-#pragma unroll
-          for (int s = 0; s < NCH; ++s) {
-            if (!wait(&v_full[vs], vp)) ok = false;
-            if (++vs == NS) { vs = 0; vp ^= 1; }
-          }
-          fence_async_proxy();                      // written by cp.async, read by the MMA
-          if (!ok || !wait(&p_full[p_count & 1], (p_count >> 1) & 1)) { ok = false; break; }
-          if (i == 1 && items_done > 0 && !wait(o_empty, (items_done - 1) & 1)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll
-          for (int s = 0; s < NCH; ++s) {
-            const uint32_t vb = base + OFF_V + vslot * SLOT;
-#pragma unroll
-            for (int ks = 0; ks < KV / 16; ++ks)
-              umma_ts(tm + TM_O, p + 8 * (s * (KV / 16) + ks), desc_at(desc_mn(KV * 128), vb + 2048 * ks), IDESC_PV,
-                      i > 1 || s > 0 || ks > 0 ? 1u : 0u);
-            umma_commit(&v_empty[vslot]);
-            if (++vslot == NS) { vslot = 0; vph ^= 1; }
-          }
-          umma_commit(&pv_done[p_count & 1]);
-          ++p_count;
-        }
+        if (!ok) break;
+        umma_commit(&s_full[count & 1]);
+        if (i == n_tiles - 1) umma_commit(q_empty);
       }
       ++items_done;
     }
     // every MMA of this warp has retired before TMEM is released (also after an
     // abort: a wait that ignores the flag)
-    umma_commit(mma_done);
-    mbar_wait_drain(mma_done, 0, a.err);
+    umma_commit(&mma_done[0]);
+    mbar_wait_drain(&mma_done[0], 0, a.err);
+  } else if (warp == W_PV) {
+    // --------------------------------------------------------------------- PV
+    int vslot = 0, vgrp = 0;
+    uint32_t vph = 0, items_done = 0, count = 0;
+    bool ok = true;
+    const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
+    };
+    for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
+      const Item it(x, w);
+      const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
+      if (n_tiles <= 0) continue;
+      if (items_done > 0 && !wait(o_empty, (items_done - 1) & 1)) { ok = false; break; }
+      for (int i = 0; i < n_tiles; ++i, ++count) {
+        const uint32_t p = tm + TM_S + 128 * (count & 1);
+        if (!wait(&p_full[count & 1], (count >> 1) & 1)) { ok = false; break; }
+#pragma unroll
+        for (int s = 0; s < NCH; ++s) {
+          if (s % GR == 0) {
+            if (!wait(&v_full[vgrp], vph)) { ok = false; break; }
+            if (++vgrp == NS) { vgrp = 0; vph ^= 1; }
+            fence_async_proxy();                    // written by cp.async, read by the MMA
+            tc_fence_after();
+          }
+          const uint32_t vb = base + OFF_V + vslot * SLOT;
+#pragma unroll
+          for (int ks = 0; ks < KV / 16; ++ks)
+            umma_ts(tm + TM_O, p + 8 * (s * (KV / 16) + ks), desc_at(desc_mn(KV * 128), vb + 2048 * ks), IDESC_PV,
+                    i > 0 || s > 0 || ks > 0 ? 1u : 0u);
+          umma_commit(&v_empty[vslot]);
+          if (++vslot == NS) vslot = 0;
+        }
+        if (!ok) break;
+        umma_commit(&pv_done[count & 1]);
+      }
+      ++items_done;
+    }
+    umma_commit(&mma_done[1]);
+    mbar_wait_drain(&mma_done[1], 0, a.err);
   } else if (warp < W_LOAD) {
     // ---------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
-    const int quad = warp & 3, half = warp >> 2;    // rows 32 quad .., scores 64 half ..
+    const int quad = warp & 3, wg = warp >> 2;      // rows 32 quad .., tiles with count % 2 == wg
     const int r = 32 * quad + lane;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-    float* xch = reinterpret_cast<float*>(smem + OFF_XCH);   // [2][2 halves][128 rows]
-    uint32_t xc = 0, count = 0, items_done = 0;
+    volatile float* m_pub = reinterpret_cast<volatile float*>(smem + OFF_XCH);      // [2][128]
+    volatile float* l_pub = m_pub + 2 * M;                                          // [2][128]
+    uint32_t count = 0, items_done = 0;             // count: tiles of the items before
     bool ok = true;
-    // hand a value to the row's other thread, and take its own
-    auto give = [&](float mine) {
-      xch[((xc & 1) * 2 + half) * M + r] = mine;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&xbar[quad]);
-    };
-    auto take = [&](float& other) -> bool {
-      const uint32_t s = (xc & 1) * 2;
-      const bool okx = __all_sync(0xffffffffu, bar_wait(&xbar[quad], xc & 1, abort_flag, a.err));
-      other = xch[(s + (half ^ 1)) * M + r];
-      ++xc;
-      return okx;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
     };
     for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
       int n_tiles, v0;                                // tiles of the item, first key number of the tile
@@ -617,85 +638,66 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
         orow = !in ? -1 : part ? w * M + r : (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
       }
       float m = -FLT_MAX, l = 0.f;
-      for (int i = 0; i < n_tiles; ++i, ++count, v0 += KT) {
-        const uint32_t buf = count & 1;
-        if (!__all_sync(0xffffffffu, bar_wait(&s_full[buf], (count >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
+      for (int i = (int)((count ^ wg) & 1); i < n_tiles; i += 2) {
+        const uint32_t n = count + i, buf = wg;     // n % 2 == wg
+        if (!wait(&s_full[buf], (n >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
         const uint32_t s_addr = tmem + lanes + TM_S + 128 * buf;
-        float s0[32], s1[32];
-        tmem_ld32(s_addr + 64 * half, s0);
-        tmem_ld32(s_addr + 64 * half + 32, s1);
+        float s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, s[q]);
         // the keys that are there, four to a byte
-        const uint4 there = *reinterpret_cast<const uint4*>(smem + OFF_OK + (count % NOK) * 32 + 16 * half);
-        const bool whole = v0 + KT - 1 <= all_max && (v0 >= all_min || v0 + KT <= a.sinks) &&
-                           (there.x & there.y & there.z & there.w) == 0x0f0f0f0fu;
-        tmem_ld_wait(s0);
-        tmem_ld_wait(s1);
+        const uint4* there = reinterpret_cast<const uint4*>(smem + OFF_OK + (n % NOK) * 32);
+        const uint4 t0 = there[0], t1 = there[1];
+        const int vt = v0 + i * KT;
+        const bool whole = vt + KT - 1 <= all_max && (vt >= all_min || vt + KT <= a.sinks) &&
+                           (t0.x & t0.y & t0.z & t0.w & t1.x & t1.y & t1.z & t1.w) == 0x0f0f0f0fu;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld_wait(s[q]);
         if (!whole) {
-          const int vb = v0 + 64 * half;
-          const uint32_t bits[4] = {there.x, there.y, there.z, there.w};
+          const uint32_t bits[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int va = vb + e, vc = va + 32;
-            const bool oka = va <= v_max && (va >= v_min || va < a.sinks) && (bits[e >> 4] >> ((e >> 2 & 3) * 8 + (e & 3)) & 1);
-            const bool okc = vc <= v_max && (vc >= v_min || vc < a.sinks) && (bits[2 + (e >> 4)] >> ((e >> 2 & 3) * 8 + (e & 3)) & 1);
-            if (!oka) s0[e] = -INFINITY;
-            if (!okc) s1[e] = -INFINITY;
+          for (int e = 0; e < KT; ++e) {
+            const int v = vt + e;
+            const bool seen = v <= v_max && (v >= v_min || v < a.sinks) && (bits[e >> 4] >> ((e >> 2 & 3) * 8 + (e & 3)) & 1);
+            if (!seen) s[e >> 5][e & 31] = -INFINITY;
           }
         }
-        // p = 2^(s scale - m) under the maximum so far, while the tile's own is
-        // found and handed over; the sum takes the fp32 values, the products p
-        // rounded to 16 bits
-        float sum;
-        uint32_t pk[32];
-        auto exps = [&]() {
-          const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-m, -m);
-          uint64_t t = pk2(0.f, 0.f);
+        float mt = -INFINITY, mu = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float x0, x1;
-            upk2(fma2(e < 16 ? pk2(s0[2 * (e & 15)], s0[2 * (e & 15) + 1]) : pk2(s1[2 * (e & 15)], s1[2 * (e & 15) + 1]),
-                      sc2, nm2), x0, x1);
-            x0 = exp2_approx(x0);
-            x1 = exp2_approx(x1);
-            t = add2(t, pk2(x0, x1));
-            pk[e] = X::pack(x0, x1);
-          }
-          float t0, t1;
-          upk2(t, t0, t1);
-          sum = t0 + t1;
-        };
-        float mt = max3f(s0[0], s1[0], s0[1]), mu = max3f(s1[1], s0[2], s1[2]);
-#pragma unroll
-        for (int e = 3; e + 1 < 32; e += 2) {
-          mt = max3f(mt, s0[e], s1[e]);
-          mu = max3f(mu, s0[e + 1], s1[e + 1]);
+        for (int e = 0; e < 32; ++e) {
+          mt = max3f(mt, s[0][e], s[1][e]);
+          mu = max3f(mu, s[2][e], s[3][e]);
         }
-        mt = max3f(mt, s0[31], s1[31]);
         mt = fmaxf(fmaxf(mt, mu) * a.scale_log2, -FLT_MAX);   // a tile without a key leaves the maximum as it is
-        give(mt);
-        if (i > 0) exps();
-        // from here on the other half has read its scores, which P overwrites
-        float other;
-        if (!take(other)) { ok = false; break; }
-        mt = fmaxf(mt, other);
+        // the maximum after the tile before, from the other group (also between
+        // items, where it is not used, so that no barrier runs two phases ahead)
+        if (n > 0) {
+          if (!wait(&hand[(wg ^ 1) * 4 + quad], ((n - 1) >> 1) & 1)) { ok = false; break; }
+        }
+        if (i > 0) {
+          const float mp = m_pub[(wg ^ 1) * M + r];
+          l *= exp2_approx(m - mp);
+          m = mp;
+        }
         const bool raise = mt > m + RAISE;
-        const bool any = __any_sync(0xffffffffu, raise);
-        if (any) {
-          const float nm = raise ? mt : m;
-          const float f = exp2_approx(m - nm);
+        const float m_old = m;
+        if (raise) m = mt;
+        m_pub[wg * M + r] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hand[wg * 4 + quad]);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = exp2_approx(m_old - m);
           l *= f;
-          m = nm;
           if (i > 0) {
             // O holds the tiles up to i - 1 once their P V is done; this tile's
             // waits for this warp
-            const uint32_t g = count - 1;
-            if (!__all_sync(0xffffffffu, bar_wait(&pv_done[g & 1], (g >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
+            if (!wait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
+            for (int cc = 0; cc < D / 16; ++cc) {
               uint32_t o[16];
-              const uint32_t ad = tmem + lanes + TM_O + (D / 2) * half + 16 * cc;
+              const uint32_t ad = tmem + lanes + TM_O + 16 * cc;
               tmem_ld16(ad, o);                     // waits for the load
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
@@ -703,9 +705,27 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
             }
           }
         }
-        if (any || i == 0) exps();
-        l += sum;
-        tmem_st32(s_addr + 32 * half, pk);
+        // p = 2^(s scale - m); the sum takes the fp32 values, the products p
+        // rounded to 16 bits.  P takes the first half of the scores' columns.
+        const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-m, -m);
+        uint64_t sum = pk2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            upk2(fma2(pk2(s[q][2 * e], s[q][2 * e + 1]), sc2, nm2), x0, x1);
+            x0 = exp2_approx(x0);
+            x1 = exp2_approx(x1);
+            sum = add2(sum, pk2(x0, x1));
+            pk[e] = X::pack(x0, x1);
+          }
+          tmem_st16(s_addr + 16 * q, pk);
+        }
+        float l0, l1;
+        upk2(sum, l0, l1);
+        l += l0 + l1;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -713,12 +733,22 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       }
       if (!ok) break;
       // ---- O / l
-      const uint32_t g = count - 1;
-      if (!__all_sync(0xffffffffu, bar_wait(&pv_done[g & 1], (g >> 1) & 1, abort_flag, a.err))) { ok = false; break; }
+      count += n_tiles;
+      const uint32_t n = count - 1;                 // the item's last tile
+      if ((n & 1) != (uint32_t)wg) {                // the other group's: its maximum is the last
+        if (!wait(&hand[(wg ^ 1) * 4 + quad], (n >> 1) & 1)) { ok = false; break; }
+        const float mp = m_pub[(wg ^ 1) * M + r];
+        l *= exp2_approx(m - mp);
+        m = mp;
+      }
+      // (this P V began after both groups had taken the item before's sums)
+      if (!wait(&pv_done[n & 1], (n >> 1) & 1)) { ok = false; break; }
       tc_fence_after();
-      float l_other;
-      give(l);
-      if (!take(l_other)) { ok = false; break; }
+      l_pub[wg * M + r] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&xbar[quad]);
+      if (!wait(&xbar[quad], items_done & 1)) { ok = false; break; }
+      const float l_other = l_pub[(wg ^ 1) * M + r];
       const float lr = l + l_other;
       const float inv = lr == 0.f ? 0.f : 1.f / lr;   // no key at all: zero
       const float lse2 = lr == 0.f ? -INFINITY : m + log2f(lr);
@@ -726,7 +756,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
 #pragma unroll 1
       for (int cc = 0; cc < D / 64; ++cc) {
         float o[32];
-        const int d0 = (D / 2) * half + 32 * cc;
+        const int d0 = (D / 2) * wg + 32 * cc;
         tmem_ld32(tmem + lanes + TM_O + d0, o);
         tmem_ld_wait(o);
         if (orow >= 0 && part) {
@@ -743,7 +773,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
                                 X::pack(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
         }
       }
-      if (orow >= 0 && half == 0) {
+      if (orow >= 0 && wg == 0) {
         if (part) sc.lse2[orow] = lse2;
         else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
       }
