@@ -155,17 +155,6 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
       ::"r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -656,11 +645,19 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
         for (int q = 0; q < 4; ++q) tmem_ld_wait(s[q]);
         if (!whole) {
           const uint32_t bits[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+          auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+          auto squeeze = [](uint32_t x) -> uint32_t {   // four bits of each byte to 16
+            x = (x | x >> 4) & 0x00ff00ffu;
+            return (x | x >> 8) & 0xffffu;
+          };
 #pragma unroll
-          for (int e = 0; e < KT; ++e) {
-            const int v = vt + e;
-            const bool seen = v <= v_max && (v >= v_min || v < a.sinks) && (bits[e >> 4] >> ((e >> 2 & 3) * 8 + (e & 3)) & 1);
-            if (!seen) s[e >> 5][e & 31] = -INFINITY;
+          for (int q = 0; q < 4; ++q) {
+            const int vq = vt + 32 * q;
+            const uint32_t mask = (squeeze(bits[2 * q]) | squeeze(bits[2 * q + 1]) << 16) & below(v_max + 1 - vq) &
+                                  (~below(v_min - vq) | below(a.sinks - vq));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(mask >> e & 1)) s[q][e] = -INFINITY;
           }
         }
         float mt = -INFINITY, mu = -INFINITY;
