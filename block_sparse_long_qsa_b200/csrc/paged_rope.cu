@@ -11,25 +11,58 @@
 namespace qsa {
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int WARPS = THREADS / 32;
-constexpr int UNROLL = 4;     // rows in flight per lane group
+constexpr int WARPS = 4;      // of a CTA
+constexpr int U = 4;          // rows of a lane group in flight
+constexpr int64_t FEW_TOKENS = 8192;
 
-// One CTA per token.  A head row is held by D / 8 lanes, 8 dims (16 bytes)
-// each; the partner of a rotary pair sits rope_dim / 16 lanes away.  The first
-// rows' loads are issued before the angles are formed, so that the two overlap.
+// A warp takes one token's rows, or with few tokens one step's rows (U per lane
+// group) of one of q, k, v.  A head row is held by D / 8 lanes, 8 dims (16 bytes)
+// each; the partner of a rotary pair sits rope_dim / 16 lanes away.  With the
+// weights folded into the rotation,
+//   y = inv (x cw + x' sw),  cw = w c,  sw = -+ w' s  (x', w': the partner's),
+// a row costs one shuffle of the raw partner words, the sum of squares, and
+// three packed operations a pair of dims.
 template <class E, int D, bool APPEND>
-__global__ void __launch_bounds__(THREADS) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+__global__ void __launch_bounds__(32 * WARPS) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int G = D / 8;                    // lanes of a row
   constexpr int RPW = 32 / G;                 // rows of a warp
-  constexpr int STEP = WARPS * RPW;
+  constexpr int STEP = RPW * U;
   using X = Elem<E>;
-  __shared__ float2 cs[128];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ float2 cs_all[WARPS][128];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % G, sub = lane / G;
-  const int64_t t = blockIdx.x;
-  const int n_q = a.q ? a.hq : 0, n_k = a.k ? a.hk : 0;
-  const int n_rows = n_q + n_k + (APPEND ? a.hk : 0);   // queries, keys, values
+  const int64_t unit = (int64_t)blockIdx.x * WARPS + warp;
+  const int64_t t = unit / a.parts;
+  if (t >= a.T) return;
+  const int part = (int)(unit - t * a.parts);
+  float2* cs = cs_all[warp];
+  const int n_q = a.q ? a.hq : 0, n_k = a.k ? a.hk : 0, n_v = APPEND ? a.hk : 0;
+
+  // this warp's rows: [q0, q1), [k0, k1), [v0, v1)
+  int q0 = 0, q1 = n_q, k0 = 0, k1 = n_k, v0 = 0, v1 = n_v;
+  if (a.parts > 1) {
+    const int pq = (n_q + STEP - 1) / STEP, pk = (n_k + STEP - 1) / STEP;
+    const int iq = part, ik = iq - pq, iv = ik - pk;
+    q0 = iq * STEP, q1 = min(q0 + STEP, n_q);             // empty where the part is another's
+    k0 = ik < 0 ? n_k : ik * STEP, k1 = min(k0 + STEP, n_k);
+    v0 = iv < 0 ? n_v : iv * STEP, v1 = min(v0 + STEP, n_v);
+  }
+
+  const uint16_t* q_row = a.q + t * a.q_ld + 8 * l;
+  const uint16_t* k_row = a.k + t * a.k_ld + 8 * l;
+  const uint16_t* v_row = a.v + t * a.v_ld + 8 * l;
+  uint4 x[U] = {};
+  auto load = [&](const uint16_t* row, int r0, int r1) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * RPW + sub;
+      if (r < r1) x[u] = *reinterpret_cast<const uint4*>(row + (int64_t)r * D);
+    }
+  };
+  // the first rows are on their way while place and angles are found
+  if (q0 < q1) load(q_row, q0, q1);
+  else if (k0 < k1) load(k_row, k0, k1);
+  else load(v_row, v0, v1);
 
   // ---- where the token goes (append)
   int64_t pos = a.pos0 + t, page_off = -1;
@@ -45,120 +78,143 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const __grid_constan
     if (L < 0) return;                        // padding
     pos = (int64_t)L + i;
     if (pos < a.kv.capacity)
-      page_off = page_row(a.kv, a.kv.table + (int64_t)b * a.kv.table_ld, (int)pos, tid == 0 ? a.err : nullptr);
-    else if (tid == 0)
+      page_off = page_row(a.kv, a.kv.table + (int64_t)b * a.kv.table_ld, (int)pos, lane == 0 ? a.err : nullptr);
+    else if (lane == 0)
       report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
   }
 
-  auto src_of = [&](int r) -> const uint16_t* {
-    if (r < n_q) return a.q + t * a.q_ld + (int64_t)r * D;
-    if (r < n_q + n_k) return a.k + t * a.k_ld + (int64_t)(r - n_q) * D;
-    return a.v + t * a.v_ld + (int64_t)(r - n_q - n_k) * D;
-  };
-  auto dst_of = [&](int r) -> uint16_t* {
-    if (r < n_q) return a.q_out + (t * a.hq + r) * D;
-    if (!APPEND) return a.k_out + (t * a.hk + (r - n_q)) * D;
-    if (page_off < 0) return nullptr;
-    const int g = r < n_q + n_k ? r - n_q : r - n_q - n_k;
-    return (r < n_q + n_k ? a.kv.k : a.kv.v) + page_off + (int64_t)g * a.kv.head_stride;
-  };
-
-  uint4 x[UNROLL] = {};
-  auto load = [&](int base) {
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const int r = base + u * STEP;
-      if (r < n_rows) x[u] = *reinterpret_cast<const uint4*>(src_of(r) + 8 * l);
-    }
-  };
-  const int r0 = warp * RPW + sub;
-  load(r0);
-
   const int half = a.rope.half;
-  for (int i = tid; i < half; i += THREADS) {
-    const int64_t p = a.positions ? (int64_t)a.positions[(int64_t)a.rope.axis[i] * a.T + t] : pos;
-    // the angle in half turns, in fp64 (far positions keep their phase), less
-    // its whole turns; what is left, at most one, has fp32's precision
-    const double turns = (double)p * a.rope.f[i];
-    const float rest = (float)(turns - 2.0 * rint(0.5 * turns));
-    float s, c;
-    sincospif(rest, &s, &c);
-    cs[i] = make_float2(a.rope.factor * c, a.rope.factor * s);
+  if (q0 < q1 || k0 < k1) {
+    for (int i = lane; i < half; i += 32) {
+      const int64_t p = a.positions ? (int64_t)a.positions[(int64_t)a.rope.axis[i] * a.T + t] : pos;
+      // the angle in half turns, in fp64 (far positions keep their phase), less
+      // its whole turns; what is left, at most one, has fp32's precision
+      const double turns = (double)p * a.rope.f[i];
+      const float rest = (float)(turns - 2.0 * rint(0.5 * turns));
+      float s, c;
+      sincospif(rest, &s, &c);
+      cs[i] = make_float2(a.rope.factor * c, a.rope.factor * s);
+    }
+    __syncwarp();
   }
-  __syncthreads();
 
-  // this lane's pairs and weights
   const int hl = half >> 3;                   // lanes of one half of the rotated dims
   const bool rot = l < 2 * hl;
   const int partner = l < hl ? l + hl : (rot ? l - hl : l);
-  const float sign = l < hl ? -1.f : 1.f;
-  float c8[8], s8[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float2 v = rot ? cs[8 * (l < hl ? l : l - hl) + e] : make_float2(1.f, 0.f);
-    c8[e] = v.x;
-    s8[e] = sign * v.y;
-  }
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (a.q_weight) wq = __ldg(reinterpret_cast<const uint4*>(a.q_weight) + l);
-  if (a.k_weight) wk = __ldg(reinterpret_cast<const uint4*>(a.k_weight) + l);
 
-  // every lane of a warp takes every step (the shuffles are warp-wide); a row
-  // past the last is computed on old registers and not stored
-  for (int w0 = warp * RPW; w0 < n_rows; w0 += STEP * UNROLL) {
-    if (w0 != warp * RPW) load(w0 + sub);
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      if (w0 + u * STEP >= n_rows) break;
-      const int r = w0 + sub + u * STEP;
-      const bool is_q = r < n_q, is_v = APPEND && r >= n_q + n_k;
-      const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float f[8];
+  // rows [r0, r1) of q or of k; x holds the first step's when loaded
+  auto turn = [&](const uint16_t* row, int r0, int r1, const uint16_t* weight, uint16_t* out, bool loaded) {
+    if (r0 >= r1) return;
+    uint64_t cw[4], sw[4];
+    {
+      uint4 wo = make_uint4(0, 0, 0, 0), wp = wo;
+      if (weight) {
+        wo = __ldg(reinterpret_cast<const uint4*>(weight) + l);
+        wp = __ldg(reinterpret_cast<const uint4*>(weight) + partner);
+      }
+      const uint32_t o[4] = {wo.x, wo.y, wo.z, wo.w}, p[4] = {wp.x, wp.y, wp.z, wp.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        f[2 * e] = X::lo(in[e]);
-        f[2 * e + 1] = X::hi(in[e]);
+        float w0 = 1.f, w1 = 1.f, p0 = 1.f, p1 = 1.f;
+        if (weight) {
+          w0 = X::lo(o[e]) + a.rope.w_plus, w1 = X::hi(o[e]) + a.rope.w_plus;
+          p0 = X::lo(p[e]) + a.rope.w_plus, p1 = X::hi(p[e]) + a.rope.w_plus;
+        }
+        float2 a0 = make_float2(1.f, 0.f), a1 = a0;
+        if (rot) {
+          const float2* c = cs + 8 * (l < hl ? l : l - hl) + 2 * e;
+          a0 = c[0], a1 = c[1];
+        }
+        const float sg = l < hl ? -1.f : 1.f;
+        cw[e] = pk2(w0 * a0.x, w1 * a1.x);
+        sw[e] = pk2(sg * p0 * a0.y, sg * p1 * a1.y);
       }
-      float ss = 0.f;
+    }
+    for (int r = r0; r < r1; r += STEP) {
+      if (!loaded) load(row, r, r1);
+      loaded = false;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-#pragma unroll
-      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
-        const float inv = rsqrtf(ss * (1.f / D) + a.rope.eps);
-        const uint32_t w[4] = {is_q ? wq.x : wk.x, is_q ? wq.y : wk.y, is_q ? wq.z : wk.z, is_q ? wq.w : wk.w};
+      for (int u = 0; u < U; ++u) {
+        if (r + u * RPW >= r1) break;
+        const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint64_t f[4], y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          f[2 * e] *= inv * (X::lo(w[e]) + a.rope.w_plus);
-          f[2 * e + 1] *= inv * (X::hi(w[e]) + a.rope.w_plus);
+          f[e] = pk2(X::lo(in[e]), X::hi(in[e]));
+          y[e] = mul2(f[e], cw[e]);
         }
-      }
-      float y[8];
+        if (half) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float o = __shfl_sync(0xffffffffu, f[e], partner, G);
-        y[e] = rot ? fmaf(o, s8[e], f[e] * c8[e]) : f[e];
+          for (int e = 0; e < 4; ++e) {
+            // lanes beyond the rotated dims add nothing, whatever they hold
+            const uint32_t o = __shfl_sync(0xffffffffu, in[e], partner, G);
+            y[e] = fma2(rot ? pk2(X::lo(o), X::hi(o)) : 0ull, sw[e], y[e]);
+          }
+        }
+        if (weight) {
+          uint64_t ss = mul2(f[0], f[0]);
+#pragma unroll
+          for (int e = 1; e < 4; ++e) ss = fma2(f[e], f[e], ss);
+          float s0, s1;
+          upk2(ss, s0, s1);
+          s0 += s1;
+#pragma unroll
+          for (int o = G / 2; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+          const float inv = rsqrtf(s0 * (1.f / D) + a.rope.eps);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], pk2(inv, inv));
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y0, y1;
+          upk2(y[e], y0, y1);
+          w[e] = X::pack(y0, y1);
+        }
+        if (out && r + u * RPW + sub < r1)
+          *reinterpret_cast<uint4*>(out + (int64_t)(r + u * RPW + sub) * (APPEND && row == k_row ? a.kv.head_stride : D)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if (r >= n_rows) continue;
-      uint16_t* dst = dst_of(r);
-      if (!dst) continue;
-      uint4 res = x[u];
-      if (!is_v)
-        res = make_uint4(X::pack(y[0], y[1]), X::pack(y[2], y[3]), X::pack(y[4], y[5]), X::pack(y[6], y[7]));
-      *reinterpret_cast<uint4*>(dst + 8 * l) = res;
+    }
+  };
+  const bool has_q = q0 < q1, has_k = k0 < k1;
+  turn(q_row, q0, q1, a.q_weight, a.q_out + t * a.hq * D + 8 * l, true);
+  uint16_t* k_out = APPEND ? (page_off >= 0 ? a.kv.k + page_off + 8 * l : nullptr) : a.k_out + t * a.hk * D + 8 * l;
+  turn(k_row, k0, k1, a.k_weight, k_out, !has_q);
+  if (APPEND && page_off >= 0) {
+    bool loaded = !has_q && !has_k;
+    for (int r = v0; r < v1; r += STEP) {
+      if (!loaded) load(v_row, r, v1);
+      loaded = false;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = r + u * RPW + sub;
+        if (h < v1) *reinterpret_cast<uint4*>(a.kv.v + page_off + (int64_t)h * a.kv.head_stride + 8 * l) = x[u];
+      }
     }
   }
+}
+
+template <class E, int D, bool APPEND>
+cudaError_t launch_one(NormRopeArgs a, cudaStream_t s) {
+  constexpr int STEP = 32 / (D / 8) * U;
+  const int n_q = a.q ? a.hq : 0, n_k = a.k ? a.hk : 0, n_v = APPEND ? a.hk : 0;
+  // a warp for each step's rows while the tokens alone do not fill the GPU
+  const int parts = (n_q + STEP - 1) / STEP + (n_k + STEP - 1) / STEP + (n_v + STEP - 1) / STEP;
+  a.parts = a.T < FEW_TOKENS ? parts : 1;
+  const int64_t warps = a.T * a.parts;
+  norm_rope_kernel<E, D, APPEND><<<(unsigned)((warps + WARPS - 1) / WARPS), 32 * WARPS, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 template <class E, bool APPEND>
 cudaError_t launch_d(const NormRopeArgs& a, int head_dim, cudaStream_t s) {
   switch (head_dim) {
-    case 64: norm_rope_kernel<E, 64, APPEND><<<(unsigned)a.T, THREADS, 0, s>>>(a); break;
-    case 128: norm_rope_kernel<E, 128, APPEND><<<(unsigned)a.T, THREADS, 0, s>>>(a); break;
-    case 256: norm_rope_kernel<E, 256, APPEND><<<(unsigned)a.T, THREADS, 0, s>>>(a); break;
+    case 64: return launch_one<E, 64, APPEND>(a, s);
+    case 128: return launch_one<E, 128, APPEND>(a, s);
+    case 256: return launch_one<E, 256, APPEND>(a, s);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

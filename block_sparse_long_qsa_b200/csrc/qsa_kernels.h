@@ -152,6 +152,7 @@ struct NormRopeArgs {
   const uint16_t* q_weight; const uint16_t* k_weight;
   uint16_t* q_out; uint16_t* k_out;
   int hq, hk;
+  int parts;                // warps to a token (set by the launcher)
   // append
   int B;
   const int32_t* cu_new; const int32_t* cache_len;
