@@ -77,7 +77,7 @@ template <class E, int D>
 __global__ void __launch_bounds__(THREADS, 1) paged_decode_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int KT = 4096 / D;                    // keys of a warp's tile
   constexpr int UNIT = WARPS * KT;
-  constexpr int G = D / 8, RPI = 32 / G;          // lanes of a row, rows of a copy instruction
+  constexpr int G = D / 8, J = KT / 4;            // 16-byte chunks of a row, rows of a lane
   constexpr int NK = KT / 8, NO = D / 8;
   using X = Elem<E>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -154,41 +154,72 @@ __global__ void __launch_bounds__(THREADS, 1) paged_decode_kernel(const __grid_c
     }
   };
 
-  // ---- loads: one tile of this warp per unit, in the order of the units
+  // ---- loads: one tile of this warp per unit, in the order of the units.  Eight
+  // lanes take 128 bytes of a row, so a lane has KT / 4 rows of a tile and knows
+  // their places by itself; their page ids are loaded a tile ahead.
+  const int c8 = lane & 7, rr = lane >> 3;
   At ia{0, 0, 0, 1};
   int64_t ix = ua;
-  if (ua < ub) ia = locate(ua);
   int islot = 0;
+  Visible iv(a, -1, nullptr);
+  const int32_t* itab = a.kv.table;
+  int ids[J];
+  auto load_ids = [&](bool new_item) {
+    if (new_item) {
+      iv = Visible(a, __ldg(a.cache_len + ia.b), nullptr);
+      itab = a.kv.table + (int64_t)ia.b * a.kv.table_ld;
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int v = min(ia.u * UNIT + warp * KT + 4 * j + rr, iv.n - 1);   // past the last: its page
+      ids[j] = __ldg(itab + page_of(a.kv, (uint32_t)min(iv.key(max(v, 0)), a.kv.capacity - 1)));
+    }
+  };
+  if (ua < ub) {
+    ia = locate(ua);
+    load_ids(true);
+  }
+  const uint32_t ring = smem_u32(smem) + warp * STAGES * SLOT;
+  const uint32_t lane_dst = rr * (D * 2) + ((c8 ^ rr) << 4);       // rows 4j + rr, j even; odd: chunk ^ 4
   auto issue = [&]() {
     if (ix < ub) {
-      const int L = __ldg(a.cache_len + ia.b);
-      const Visible vis(a, L, nullptr);
-      const int32_t* table = a.kv.table + (int64_t)ia.b * a.kv.table_ld;
-      const int v0 = ia.u * UNIT + warp * KT;
-      const int64_t head = (int64_t)(ia.hm / MT) * a.kv.head_stride;
-      // this lane's row (two rows for KT = 64) of the tile
-      int64_t off[(KT + 31) / 32];
-      uint64_t ok = 0;
+      const int v0 = ia.u * UNIT + warp * KT + rr;
+      const int64_t head = (int64_t)(ia.hm / MT) * a.kv.head_stride + 8 * c8;
+      const uint32_t kd = ring + islot * SLOT;
+      uint32_t ok = 0;                                              // bit j: row 4j + rr
+      bool bad = false;
 #pragma unroll
-      for (int h = 0; h < (KT + 31) / 32; ++h) {
-        const int r = 32 * h + lane, v = v0 + r;
-        off[h] = r < KT && v < vis.n ? page_row(a.kv, table, vis.key(v), a.err) : -1;
-        ok |= (uint64_t)__ballot_sync(0xffffffffu, off[h] >= 0) << (32 * h);
-        off[h] += head;                            // a row that is not there stays unread
-      }
-      if (lane == 0) vmask[warp * STAGES + islot] = ok;
-      const uint32_t kd = smem_u32(smem) + (warp * STAGES + islot) * SLOT, vd = kd + KT * D * 2;
-      const int c = lane % G;
+      for (int j = 0; j < J; ++j) {
+        const int v = v0 + 4 * j, key = iv.key(v);
+        const bool there = v < iv.n, good = there && (uint32_t)ids[j] < (uint32_t)a.kv.n_pages;
+        bad |= there && !good;
+        ok |= (uint32_t)good << j;
+        const int in_page = key - (int)(page_of(a.kv, (uint32_t)key) * (uint32_t)a.kv.page_size);
+        const int64_t off = good ? (int64_t)ids[j] * a.kv.page_stride + (int64_t)in_page * a.kv.token_stride + head : 0;
+        const uint32_t dst = kd + (lane_dst ^ ((j & 1) << 6)) + 4 * j * (D * 2);
+        const uint16_t* ks = a.kv.k + off;
+        const uint16_t* vs = a.kv.v + off;
 #pragma unroll
-      for (int j = 0; j < KT / RPI; ++j) {
-        const int row = j * RPI + lane / G;
-        const int64_t o = __shfl_sync(0xffffffffu, off[j * RPI / 32], row & 31) + 8 * c;
-        const bool valid = (ok >> row) & 1;
-        cp_async16_zfill(kd + row_chunk<D>(row, c), valid ? a.kv.k + o : a.kv.k, valid);
-        cp_async16_zfill(vd + row_chunk<D>(row, c), valid ? a.kv.v + o : a.kv.v, valid);
+        for (int ch = 0; ch < D / 64; ++ch) {
+          cp_async16_zfill(dst + 128 * ch, ks + 64 * ch, good);
+          cp_async16_zfill(dst + KT * D * 2 + 128 * ch, vs + 64 * ch, good);
+        }
       }
+      if (bad) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
+      uint64_t mask = ~0ull;
+      if (!__all_sync(0xffffffffu, ok == (1u << J) - 1)) {
+        mask = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const uint32_t b = __ballot_sync(0xffffffffu, ok >> j & 1);   // eight lanes a row
+          mask |= (uint64_t)((b & 1) | (b >> 7 & 2) | (b >> 14 & 4) | (b >> 21 & 8)) << (4 * j);
+        }
+      }
+      if (lane == 0) vmask[warp * STAGES + islot] = mask;
       ++ix;
-      if (++ia.u == ia.nu) next_item(ia);
+      bool next = ++ia.u == ia.nu;
+      if (next) next_item(ia);
+      if (ix < ub) load_ids(next);
       if (++islot == STAGES) islot = 0;
     }
     cp_async_commit();
@@ -199,7 +230,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_decode_kernel(const __grid_c
   // ---- products
   const uint32_t q_base = smem_u32(smem) + OFF_Q;
   int slot = 0;
-  At ca = ia;
+  At ca{0, 0, 0, 1};
   if (ua < ub) ca = locate(ua);
   for (int64_t x = ua; x < ub;) {
     const int n_units = (int)min((int64_t)(ca.nu - ca.u), ub - x);
@@ -247,8 +278,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_decode_kernel(const __grid_c
             X::mma(s[n + 1], qa, kb[2], kb[3]);
           }
         }
-        const uint64_t full = KT == 64 ? ~0ull : (1ull << (KT & 63)) - 1;
-        if (ok != full) {
+        if (ok != ~0ull) {
 #pragma unroll
           for (int n = 0; n < NK; ++n)
 #pragma unroll

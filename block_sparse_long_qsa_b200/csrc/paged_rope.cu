@@ -11,9 +11,15 @@
 namespace qsa {
 namespace {
 
-constexpr int WARPS = 4;      // of a CTA
-constexpr int U = 4;          // rows of a lane group in flight
-constexpr int64_t FEW_TOKENS = 8192;
+// Warps of a CTA: one, so that a warp's place is taken as soon as it is done (32K
+// tokens of 24 + 2 heads of 256: 136 us, with two warps 145, with four 146).
+constexpr int WARPS = 1;
+// Rows of a lane group in flight (32K tokens: 2 rows 148 us, 4 rows 136, 6 rows 138).
+constexpr int U = 4;
+// Below this many tokens a token's rows are spread over several warps (26 rows
+// of 256: 2048 tokens 13.7 us against 15.3 with a warp a token, 4096 tokens 24.1
+// against 21.2).
+constexpr int64_t FEW_TOKENS = 3000;
 
 // A warp takes one token's rows, or with few tokens one step's rows (U per lane
 // group) of one of q, k, v.  A head row is held by D / 8 lanes, 8 dims (16 bytes)
