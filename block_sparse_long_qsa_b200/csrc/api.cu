@@ -1123,6 +1123,8 @@ qsa_status check_kv(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B
   if (kv->n_pages <= 0 || kv->page_size <= 0 || kv->max_pages <= 0 || kv->table_ld < kv->max_pages)
     return QSA_ERR_INVALID_ARG;
   if (kv->n_pages > INT32_MAX || kv->page_size > 65536) return QSA_ERR_UNSUPPORTED;
+  const int64_t most = (int64_t)1 << 34;             // strides fit 32 bits in 16-byte units
+  if (kv->page_stride >= most || kv->token_stride >= most || kv->head_stride >= most) return QSA_ERR_UNSUPPORTED;
   if (!stride_ok(kv->page_stride, p->head_dim) || !stride_ok(kv->token_stride, p->head_dim) ||
       !stride_ok(kv->head_stride, p->head_dim))
     return QSA_ERR_INVALID_ARG;

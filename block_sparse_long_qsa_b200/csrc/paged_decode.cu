@@ -7,15 +7,16 @@
 // against the sequence's visible keys.  Bound by HBM: K and V are read once,
 // 4 D bytes a key against 4 D flops a query head.
 //
-// Split: all items' visible keys are laid end to end in units of 4 KT keys and
+// Split: all items' visible keys are laid end to end in units of a tile a warp and
 // cut evenly over the CTAs (one to an SM), so a batch of any mix of lengths
 // keeps every SM busy to the last unit.  A CTA's piece of an item that it
 // shares with others goes to the scratch as normalised fp32 rows with their
 // log-sum-exp; the join kernel adds the pieces in the order of the keys.
 //
-// Tiles: each of the 4 warps streams its own KT = 4096 / D keys of a unit (K and
-// V 16 KB) through its own ring of three slots with cp.async, so no barrier
-// stands between loads and products, and up to 192 KB an SM are in flight.  The
+// Tiles: each warp streams its own KT keys of a unit (head dim 256: 4 warps of 16
+// keys; else 8 warps of 2048 / D) through its own ring of three slots with
+// cp.async, so no barrier stands between loads and products, and up to 192 KB an
+// SM are in flight.  The
 // rows are few (M = 16 of mma.sync; a tcgen05 tile of 128 rows would be mostly
 // padding) and the products take a third of the time of the loads.
 #include <cfloat>
@@ -25,18 +26,21 @@
 namespace qsa {
 namespace {
 
-constexpr int WARPS = 4;
-constexpr int THREADS = 32 * WARPS;
 constexpr int STAGES = 3;
-constexpr int SLOT = 16384;                       // K and V of KT keys
+constexpr int MAX_WARPS = 8;
+// Warps of a CTA and bytes of a slot (K and V of KT keys): eight warps hide the
+// products' latencies better than four; head dim 256 has four, since a tile of 16
+// keys fills 16 KB there.
+__host__ __device__ constexpr int warps_of(int D) { return D == 256 ? 4 : 8; }
+constexpr int RING = 196608;                      // all slots
 constexpr int ROWS = 16;
 constexpr int MAX_CTAS = 160;                     // bound of the scratch (148 SMs on B200)
 constexpr int MAX_B = 4096;
-constexpr uint32_t OFF_Q = WARPS * STAGES * SLOT; // 16 rows of queries
+constexpr uint32_t OFF_Q = RING;                  // 16 rows of queries
 constexpr uint32_t OFF_P = OFF_Q + ROWS * 512;    // running units of the sequences, MAX_B + 1
 constexpr uint32_t OFF_V = OFF_P + 4 * (MAX_B + 4);
-constexpr uint32_t OFF_ML = OFF_V + WARPS * STAGES * 8;   // valid rows of each slot above
-constexpr uint32_t SMEM = OFF_ML + WARPS * ROWS * 8 + 64;
+constexpr uint32_t OFF_ML = OFF_V + MAX_WARPS * STAGES * 8;   // valid rows of each slot above
+constexpr uint32_t SMEM = OFF_ML + MAX_WARPS * ROWS * 8 + 64;
 static_assert(SMEM <= 232448, "decode smem");
 
 // What CTA c leaves for the join: the item that starts in its range and goes on
@@ -74,10 +78,13 @@ struct Visible {
 };
 
 template <class E, int D>
-__global__ void __launch_bounds__(THREADS, 1) paged_decode_kernel(const __grid_constant__ PagedAttnArgs a) {
-  constexpr int KT = 4096 / D;                    // keys of a warp's tile
+__global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const __grid_constant__ PagedAttnArgs a) {
+  constexpr int WARPS = warps_of(D), THREADS = 32 * WARPS;
+  constexpr int SLOT = RING / (WARPS * STAGES), KT = SLOT / (4 * D);   // a warp's tile
   constexpr int UNIT = WARPS * KT;
-  constexpr int G = D / 8, J = KT / 4;            // 16-byte chunks of a row, rows of a lane
+  constexpr int G = D / 8;                        // 16-byte chunks of a row
+  // copies: LPR lanes a row at a time, so a lane has J rows of a tile, each in CC steps
+  constexpr int LPR = D == 256 ? 8 : 4, RPI = 32 / LPR, J = KT / RPI, CC = G / LPR;
   constexpr int NK = KT / 8, NO = D / 8;
   using X = Elem<E>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -154,10 +161,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_decode_kernel(const __grid_c
     }
   };
 
-  // ---- loads: one tile of this warp per unit, in the order of the units.  Eight
-  // lanes take 128 bytes of a row, so a lane has KT / 4 rows of a tile and knows
-  // their places by itself; their page ids are loaded a tile ahead.
-  const int c8 = lane & 7, rr = lane >> 3;
+  // ---- loads: one tile of this warp per unit, in the order of the units.  Few
+  // lanes share a row, so a lane has few rows of a tile and finds their places by
+  // itself; their page ids are loaded a tile ahead.
+  const int cl = lane % LPR, rr = lane / LPR;
   At ia{0, 0, 0, 1};
   int64_t ix = ua;
   int islot = 0;
@@ -171,7 +178,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_decode_kernel(const __grid_c
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int v = min(ia.u * UNIT + warp * KT + 4 * j + rr, iv.n - 1);   // past the last: its page
+      const int v = min(ia.u * UNIT + warp * KT + RPI * j + rr, iv.n - 1);   // past the last: its page
       ids[j] = __ldg(itab + page_of(a.kv, (uint32_t)min(iv.key(max(v, 0)), a.kv.capacity - 1)));
     }
   };
@@ -180,40 +187,54 @@ __global__ void __launch_bounds__(THREADS, 1) paged_decode_kernel(const __grid_c
     load_ids(true);
   }
   const uint32_t ring = smem_u32(smem) + warp * STAGES * SLOT;
-  const uint32_t lane_dst = rr * (D * 2) + ((c8 ^ rr) << 4);       // rows 4j + rr, j even; odd: chunk ^ 4
+  // strides in 16-byte units fit 32 bits (checked on the host)
+  const uint32_t page16 = (uint32_t)(a.kv.page_stride >> 3), token16 = (uint32_t)(a.kv.token_stride >> 3);
+  // row RPI j + rr, chunk LPR cc + cl: row_chunk's exchange is (cl ^ rr) and a 4
+  // for every other j (eight lanes a row) or cc (four)
+  const uint32_t lane_dst = rr * (D * 2) + ((cl ^ rr) << 4);
   auto issue = [&]() {
     if (ix < ub) {
       const int v0 = ia.u * UNIT + warp * KT + rr;
-      const int64_t head = (int64_t)(ia.hm / MT) * a.kv.head_stride + 8 * c8;
       const uint32_t kd = ring + islot * SLOT;
-      uint32_t ok = 0;                                              // bit j: row 4j + rr
+      const int64_t head = (int64_t)(ia.hm / MT) * a.kv.head_stride + 8 * cl;
+      const uint16_t* kh = a.kv.k + head;
+      const uint16_t* vh = a.kv.v + head;
+      uint32_t ok = 0;                                              // bit j: row RPI j + rr
       bool bad = false;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const int v = v0 + 4 * j, key = iv.key(v);
+        const int v = v0 + RPI * j, key = iv.key(v);
         const bool there = v < iv.n, good = there && (uint32_t)ids[j] < (uint32_t)a.kv.n_pages;
         bad |= there && !good;
         ok |= (uint32_t)good << j;
-        const int in_page = key - (int)(page_of(a.kv, (uint32_t)key) * (uint32_t)a.kv.page_size);
-        const int64_t off = good ? (int64_t)ids[j] * a.kv.page_stride + (int64_t)in_page * a.kv.token_stride + head : 0;
-        const uint32_t dst = kd + (lane_dst ^ ((j & 1) << 6)) + 4 * j * (D * 2);
-        const uint16_t* ks = a.kv.k + off;
-        const uint16_t* vs = a.kv.v + off;
+        const uint32_t in_page = (uint32_t)key - page_of(a.kv, (uint32_t)key) * (uint32_t)a.kv.page_size;
+        const uint64_t off = good ? ((uint64_t)(uint32_t)ids[j] * page16 + (uint64_t)in_page * token16) << 3 : 0;
 #pragma unroll
-        for (int ch = 0; ch < D / 64; ++ch) {
-          cp_async16_zfill(dst + 128 * ch, ks + 64 * ch, good);
-          cp_async16_zfill(dst + KT * D * 2 + 128 * ch, vs + 64 * ch, good);
+        for (int cc = 0; cc < CC; ++cc) {
+          const uint32_t dst = kd + (lane_dst ^ ((LPR == 8 ? j & 1 : cc & 1) << 6)) + RPI * j * (D * 2) +
+                               (LPR * cc / 8) * 128;
+          cp_async16_zfill(dst, kh + off + 8 * LPR * cc, good);
+          cp_async16_zfill(dst + KT * D * 2, vh + off + 8 * LPR * cc, good);
         }
       }
       if (bad) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
       uint64_t mask = ~0ull;
-      if (!__all_sync(0xffffffffu, ok == (1u << J) - 1)) {
+      if (!__all_sync(0xffffffffu, ok == (uint32_t)((1ull << J) - 1))) {
         mask = 0;
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const uint32_t b = __ballot_sync(0xffffffffu, ok >> j & 1);   // eight lanes a row
-          mask |= (uint64_t)((b & 1) | (b >> 7 & 2) | (b >> 14 & 4) | (b >> 21 & 8)) << (4 * j);
+        for (int j = 0; j < J; ++j) {                               // one bit of each row's lanes, side by side
+          uint32_t b = __ballot_sync(0xffffffffu, ok >> j & 1);
+          if (LPR == 8) {
+            b = (b & 1) | (b >> 7 & 2) | (b >> 14 & 4) | (b >> 21 & 8);
+          } else {
+            b &= 0x11111111u;
+            b = (b | b >> 3) & 0x03030303u;
+            b = (b | b >> 6) & 0x000f000fu;
+            b = (b | b >> 12) & 0xffu;
+          }
+          mask |= (uint64_t)b << (RPI * j);
         }
+        if (KT < 64) mask |= ~0ull << (KT & 63);
       }
       if (lane == 0) vmask[warp * STAGES + islot] = mask;
       ++ix;
@@ -259,12 +280,15 @@ __global__ void __launch_bounds__(THREADS, 1) paged_decode_kernel(const __grid_c
       __syncwarp();
       const uint64_t ok = vmask[warp * STAGES + slot];
       const uint32_t kd = smem_u32(smem) + (warp * STAGES + slot) * SLOT, vd = kd + KT * D * 2;
-      if (ok) {
-        float s[NK][4];
+      // (bits past the tile are set; no key at all: nothing to add)
+      if (KT == 64 ? ok != 0 : (ok & ((1ull << (KT & 63)) - 1)) != 0) {
+        // two sums a score where a tile has few: shorter chains of products
+        constexpr int CH = NK == 2 ? 2 : 1;
+        float sp[CH][NK][4];
 #pragma unroll
-        for (int n = 0; n < NK; ++n)
+        for (int n = 0; n < CH * NK; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+          for (int e = 0; e < 4; ++e) sp[n / NK][n % NK][e] = 0.f;
         const uint32_t qr = (lane & 7) + ((lane >> 3) & 1) * 8, kr = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -274,10 +298,16 @@ __global__ void __launch_bounds__(THREADS, 1) paged_decode_kernel(const __grid_c
           for (int n = 0; n < NK; n += 2) {
             uint32_t kb[4];
             ldsm4(kb, kd + row_chunk<D>(8 * n + kr, 2 * ks + ((lane >> 3) & 1)));
-            X::mma(s[n], qa, kb[0], kb[1]);
-            X::mma(s[n + 1], qa, kb[2], kb[3]);
+            X::mma(sp[ks % CH][n], qa, kb[0], kb[1]);
+            X::mma(sp[ks % CH][n + 1], qa, kb[2], kb[3]);
           }
         }
+        float (&s)[NK][4] = sp[0];
+        if (CH == 2)
+#pragma unroll
+          for (int n = 0; n < NK; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] += sp[CH - 1][n][e];
         if (ok != ~0ull) {
 #pragma unroll
           for (int n = 0; n < NK; ++n)
@@ -486,7 +516,7 @@ cudaError_t launch_d(const PagedAttnArgs& a, int num_sms, cudaStream_t s, bool j
       if (e != cudaSuccess) return e;
       if (dev < 64) attr_done[dev] = true;
     }
-    paged_decode_kernel<E, D><<<grid, THREADS, SMEM, s>>>(a);
+    paged_decode_kernel<E, D><<<grid, 32 * warps_of(D), SMEM, s>>>(a);
     return cudaGetLastError();
   }
   const int per = a.hq / a.hk;

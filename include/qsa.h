@@ -436,7 +436,7 @@ void qsa_default_layer_params(qsa_layer_params* p);
  * j / page_size], slot j % page_size; its row of KV head g starts at element
  *   page * page_stride + slot * token_stride + g * head_stride
  * of k_pages and of v_pages.  Strides are in elements, multiples of 8, at least
- * head_dim; both pointers are 16-byte aligned.  So token-major pages
+ * head_dim and below 2^34; both pointers are 16-byte aligned.  So token-major pages
  * [n_pages][page_size][n_kv][head_dim], head-major ones, and pages that hold K
  * and V side by side all fit.  page_size: any, 1 .. 65536.  Pages may be shared
  * by sequences as long as no call appends to a shared page. */
