@@ -328,7 +328,15 @@ def qsa_decode_noalloc(p: qsa_params, B: int, max_len: int, cache_len, k_cache, 
 
 
 # ------------------------------------------------- layers over a paged cache
-_TORCH_DTYPE = {DTYPE_BF16: (torch.bfloat16, torch.uint16), DTYPE_FP16: (torch.float16, torch.uint16)}
+def _raw_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# torch's own C entries where it has them: the public functions wrap them in
+# Python (about 2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_ELEMENT = (torch.bfloat16, torch.float16)     # by qsa_layer_params.dtype
 
 
 def layer_params(n_q_heads: int = 24, n_kv_heads: int = 2, head_dim: int = 256, dtype=torch.bfloat16,
@@ -379,77 +387,87 @@ class PagedKV:
         d = k_pages.shape[3]
         st = [s if n > 1 else max(d, s) // 8 * 8 for n, s in zip(k_pages.shape, k_pages.stride())]
         ld = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+        self.heads, self.dtype = tuple(k_pages.shape[2:]), k_pages.dtype
+        self.rows, self.device = page_table.shape[0], k_pages.get_device()
         self.c = qsa_paged_kv(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[0], k_pages.shape[1],
                               page_table.shape[1], st[0], st[1], st[2], page_table.data_ptr(), ld)
+        self.ref = ctypes.byref(self.c)
 
 
-def _rows(t, what: str, p: qsa_layer_params, T: int, H: int, like):
-    """(pointer, row stride) of a [T][H][head_dim] tensor whose rows are contiguous inside."""
-    if t is None:
-        return None, 0
-    D = p.head_dim
-    if t.dim() != 3 or t.shape[0] < T or t.shape[1] != H or t.shape[2] != D:
-        raise ValueError(f"{what} must be [{T}][{H}][{D}], not {list(t.shape)}")
-    if t.dtype not in _TORCH_DTYPE[p.dtype]:
-        raise ValueError(f"{what} has dtype {t.dtype}, the layer {_TORCH_DTYPE[p.dtype][0]}")
-    if t.device != like:
-        raise ValueError(f"{what} is on {t.device}, not on {like}")
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
-        raise ValueError(f"the heads of a row of {what} must be contiguous")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else H * D)
-
-
-def _flat(t, what: str, shape, dtypes, like):
-    """Pointer of a contiguous tensor of the given shape (rows may be more)."""
+def _flat(t, what: str, shape, dt, dev: int):
+    """Pointer of a contiguous tensor of the given shape (rows may be more),
+    dtype (``dt``, or bit patterns in torch.uint16 for a 16-bit one) and device
+    index; None for None."""
     if t is None:
         return None
-    if t.dim() != len(shape) or t.shape[0] < shape[0] or tuple(t.shape[1:]) != tuple(shape[1:]):
-        raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{what} has dtype {t.dtype}, not {dtypes[0]}")
-    if t.device != like:
-        raise ValueError(f"{what} is on {t.device}, not on {like}")
-    if not t.is_contiguous():
-        raise ValueError("QSA tensors must be contiguous")
+    if t.shape != shape or t.dtype is not dt or t.get_device() != dev or not t.is_contiguous():
+        if t.dim() != len(shape) or t.shape[0] < shape[0] or tuple(t.shape[1:]) != shape[1:]:
+            raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
+        if t.dtype is not dt and not (t.dtype is torch.uint16 and dt in _ELEMENT):
+            raise ValueError(f"{what} has dtype {t.dtype}, not {dt}")
+        if t.get_device() != dev:
+            raise ValueError(f"{what} is on {t.device}, not on the device of the other tensors")
+        if not t.is_contiguous():
+            raise ValueError("QSA tensors must be contiguous")
     return t.data_ptr()
 
 
-_I32 = (torch.int32,)
-_F32 = (torch.float32,)
+def _rows(t, what: str, T: int, H: int, D: int, dt, dev: int):
+    """(pointer, row stride) of a [T][H][D] tensor whose rows are contiguous inside."""
+    if t is None:
+        return None, 0
+    st = t.stride()
+    if t.shape != (T, H, D) or t.dtype is not dt or t.get_device() != dev or st[2] != 1 or st[1] != D or T < 2:
+        if t.dim() != 3 or t.shape[0] < T or t.shape[1] != H or t.shape[2] != D:
+            raise ValueError(f"{what} must be [{T}][{H}][{D}], not {list(t.shape)}")
+        if t.dtype is not dt and t.dtype is not torch.uint16:
+            raise ValueError(f"{what} has dtype {t.dtype}, the layer {dt}")
+        if t.get_device() != dev:
+            raise ValueError(f"{what} is on {t.device}, not on the device of the other tensors")
+        if st[2] != 1 or (H > 1 and st[1] != D):
+            raise ValueError(f"the heads of a row of {what} must be contiguous")
+        if t.shape[0] < 2:
+            return t.data_ptr(), H * D          # the stride of a single row is never used
+    return t.data_ptr(), st[0]
 
 
-def _positions(positions, p, T, like):
+def _positions(positions, axes: int, T: int, dev: int):
     if positions is None:
         return None
-    if p.rope_axes == 1 and positions.dim() == 1:
+    if axes == 1 and positions.dim() == 1:
         positions = positions[None]
-    if tuple(positions.shape) != (p.rope_axes, T):
-        raise ValueError(f"positions must be [{p.rope_axes}][{T}], not {list(positions.shape)}")
-    return _flat(positions, "positions", (p.rope_axes, T), _I32, like)
+    if positions.shape != (axes, T):
+        raise ValueError(f"positions must be [{axes}][{T}], not {list(positions.shape)}")
+    return _flat(positions, "positions", (axes, T), torch.int32, dev)
 
 
-def _paged(p, kv: PagedKV, B: int, ws):
-    """Checks of the cache against the layer; the cache's device."""
-    if kv.k_pages.shape[2] != p.n_kv_heads or kv.k_pages.shape[3] != p.head_dim:
-        raise ValueError(f"the pages hold {list(kv.k_pages.shape[2:])}, the layer [{p.n_kv_heads}, {p.head_dim}]")
-    if kv.k_pages.dtype not in _TORCH_DTYPE[p.dtype]:
-        raise ValueError(f"the pages have dtype {kv.k_pages.dtype}, the layer {_TORCH_DTYPE[p.dtype][0]}")
-    if kv.page_table.shape[0] < B:
-        raise ValueError(f"page_table has {kv.page_table.shape[0]} rows for {B} sequences")
-    dev = kv.k_pages.device
-    if ws is None or ws.device != dev or not ws.is_contiguous():
+def _paged(p, kv: "PagedKV", B: int, ws):
+    """Checks of the cache against the layer; (device index, element type, workspace pointer and bytes)."""
+    dt = _ELEMENT[p.dtype]
+    if kv.heads != (p.n_kv_heads, p.head_dim):
+        raise ValueError(f"the pages hold {list(kv.heads)}, the layer [{p.n_kv_heads}, {p.head_dim}]")
+    if kv.dtype is not dt and kv.dtype is not torch.uint16:
+        raise ValueError(f"the pages have dtype {kv.dtype}, the layer {dt}")
+    if kv.rows < B:
+        raise ValueError(f"page_table has {kv.rows} rows for {B} sequences")
+    if ws is None or ws.get_device() != kv.device or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous workspace on the cache's device (paged_workspace)")
-    return dev
+    return kv.device, dt, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _on(dev, stream, call, where: str):
-    """``call(stream pointer)`` with ``dev`` current, on ``stream`` or on that device's current stream."""
-    if dev.type != "cuda":
-        raise ValueError(f"{where}: tensors are on {dev}, not on a CUDA device")
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return _check(call(_stream(stream)), where)
-    with torch.cuda.device(dev):
-        return _check(call(_stream(stream)), where)
+def _run(fn: str, dev: int, stream, *args):
+    """The C call ``fn`` with ``dev`` current, on ``stream`` or on that device's current stream."""
+    if dev < 0:
+        raise ValueError(f"{fn}: the tensors are not on a CUDA device")
+    f = getattr(_lib or load(), fn)
+    s = stream.cuda_stream if stream is not None else _raw_stream(dev)
+    if dev == _current_device():
+        rc = f(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, s)
+    if rc != QSA_OK:
+        _check(rc, fn)
 
 
 def qsa_norm_rope(p: qsa_layer_params, T: int, pos0: int, q, k, q_weight, k_weight, q_out, k_out, positions=None,
@@ -457,54 +475,51 @@ def qsa_norm_rope(p: qsa_layer_params, T: int, pos0: int, q, k, q_weight, k_weig
     """``q`` [T][n_q_heads][head_dim], ``k`` [T][n_kv_heads][head_dim] (row
     strides free); ``q`` with ``q_out``, or ``k`` with ``k_out``, and each weight
     may be None; ``positions`` int32 [rope_axes][T]."""
-    like = (q if q is not None else k).device
-    w = _TORCH_DTYPE[p.dtype]
-    (qp, ql), (kp, kl) = _rows(q, "q", p, T, p.n_q_heads, like), _rows(k, "k", p, T, p.n_kv_heads, like)
-    args = (_positions(positions, p, T, like), qp, ql, kp, kl, _flat(q_weight, "q_weight", (p.head_dim,), w, like),
-            _flat(k_weight, "k_weight", (p.head_dim,), w, like),
-            _flat(q_out, "q_out", (T, p.n_q_heads, p.head_dim), w, like),
-            _flat(k_out, "k_out", (T, p.n_kv_heads, p.head_dim), w, like))
-    _on(like, stream, lambda s: load().qsa_norm_rope(ctypes.byref(p), T, pos0, *args, s), "qsa_norm_rope")
+    if q is None and k is None:
+        raise ValueError("one of q and k is needed")
+    dev, dt = (q if q is not None else k).get_device(), _ELEMENT[p.dtype]
+    H, G, D = p.n_q_heads, p.n_kv_heads, p.head_dim
+    qp, ql = _rows(q, "q", T, H, D, dt, dev)
+    kp, kl = _rows(k, "k", T, G, D, dt, dev)
+    _run("qsa_norm_rope", dev, stream, ctypes.byref(p), T, pos0, _positions(positions, p.rope_axes, T, dev), qp, ql, kp,
+         kl, _flat(q_weight, "q_weight", (D,), dt, dev), _flat(k_weight, "k_weight", (D,), dt, dev),
+         _flat(q_out, "q_out", (T, H, D), dt, dev), _flat(k_out, "k_out", (T, G, D), dt, dev))
 
 
 def qsa_paged_append(p: qsa_layer_params, kv: PagedKV, B: int, T: int, cu_new, cache_len, k, v, ws, q=None, q_out=None,
                      q_weight=None, k_weight=None, positions=None, stream=None):
     """``cu_new`` int32 [B + 1] or None (one token per sequence), ``cache_len``
     int32 [B], both on the device."""
-    dev = _paged(p, kv, B, ws)
-    w = _TORCH_DTYPE[p.dtype]
-    (qp, ql), (kp, kl) = _rows(q, "q", p, T, p.n_q_heads, dev), _rows(k, "k", p, T, p.n_kv_heads, dev)
-    vp, vl = _rows(v, "v", p, T, p.n_kv_heads, dev)
-    args = (_flat(cu_new, "cu_new", (B + 1,), _I32, dev), _flat(cache_len, "cache_len", (B,), _I32, dev),
-            _positions(positions, p, T, dev), qp, ql, kp, kl, vp, vl,
-            _flat(q_weight, "q_weight", (p.head_dim,), w, dev), _flat(k_weight, "k_weight", (p.head_dim,), w, dev),
-            _flat(q_out, "q_out", (T, p.n_q_heads, p.head_dim), w, dev), ws.data_ptr(),
-            ws.numel() * ws.element_size())
-    _on(dev, stream, lambda s: load().qsa_paged_append(ctypes.byref(p), ctypes.byref(kv.c), B, T, *args, s),
-        "qsa_paged_append")
+    dev, dt, wp, wb = _paged(p, kv, B, ws)
+    H, G, D = p.n_q_heads, p.n_kv_heads, p.head_dim
+    qp, ql = _rows(q, "q", T, H, D, dt, dev)
+    kp, kl = _rows(k, "k", T, G, D, dt, dev)
+    vp, vl = _rows(v, "v", T, G, D, dt, dev)
+    _run("qsa_paged_append", dev, stream, ctypes.byref(p), kv.ref, B, T,
+         _flat(cu_new, "cu_new", (B + 1,), torch.int32, dev), _flat(cache_len, "cache_len", (B,), torch.int32, dev),
+         _positions(positions, p.rope_axes, T, dev), qp, ql, kp, kl, vp, vl,
+         _flat(q_weight, "q_weight", (D,), dt, dev), _flat(k_weight, "k_weight", (D,), dt, dev),
+         _flat(q_out, "q_out", (T, H, D), dt, dev), wp, wb)
 
 
 def qsa_paged_decode(p: qsa_layer_params, kv: PagedKV, B: int, cache_len, q, out, ws, lse=None, stream=None):
     """One new token per sequence (``q``, ``out`` [B][n_q_heads][head_dim])."""
-    dev = _paged(p, kv, B, ws)
-    w, shape = _TORCH_DTYPE[p.dtype], (B, p.n_q_heads, p.head_dim)
-    args = (_flat(cache_len, "cache_len", (B,), _I32, dev), _flat(q, "q", shape, w, dev),
-            _flat(out, "out", shape, w, dev), _flat(lse, "lse", shape[:2], _F32, dev), ws.data_ptr(),
-            ws.numel() * ws.element_size())
-    _on(dev, stream, lambda s: load().qsa_paged_decode(ctypes.byref(p), ctypes.byref(kv.c), B, *args, s),
-        "qsa_paged_decode")
+    dev, dt, wp, wb = _paged(p, kv, B, ws)
+    H, D = p.n_q_heads, p.head_dim
+    _run("qsa_paged_decode", dev, stream, ctypes.byref(p), kv.ref, B,
+         _flat(cache_len, "cache_len", (B,), torch.int32, dev), _flat(q, "q", (B, H, D), dt, dev),
+         _flat(out, "out", (B, H, D), dt, dev), _flat(lse, "lse", (B, H), torch.float32, dev), wp, wb)
 
 
 def qsa_paged_prefill(p: qsa_layer_params, kv: PagedKV, B: int, T: int, cu_new, cache_len, q, out, ws, lse=None,
                       stream=None):
     """T new tokens of B sequences (``q``, ``out`` [T][n_q_heads][head_dim])."""
-    dev = _paged(p, kv, B, ws)
-    w, shape = _TORCH_DTYPE[p.dtype], (T, p.n_q_heads, p.head_dim)
-    args = (_flat(cu_new, "cu_new", (B + 1,), _I32, dev), _flat(cache_len, "cache_len", (B,), _I32, dev),
-            _flat(q, "q", shape, w, dev), _flat(out, "out", shape, w, dev), _flat(lse, "lse", shape[:2], _F32, dev),
-            ws.data_ptr(), ws.numel() * ws.element_size())
-    _on(dev, stream, lambda s: load().qsa_paged_prefill(ctypes.byref(p), ctypes.byref(kv.c), B, T, *args, s),
-        "qsa_paged_prefill")
+    dev, dt, wp, wb = _paged(p, kv, B, ws)
+    H, D = p.n_q_heads, p.head_dim
+    _run("qsa_paged_prefill", dev, stream, ctypes.byref(p), kv.ref, B, T,
+         _flat(cu_new, "cu_new", (B + 1,), torch.int32, dev), _flat(cache_len, "cache_len", (B,), torch.int32, dev),
+         _flat(q, "q", (T, H, D), dt, dev), _flat(out, "out", (T, H, D), dt, dev),
+         _flat(lse, "lse", (T, H), torch.float32, dev), wp, wb)
 
 
 def qsa_paged_workspace_size(p: qsa_layer_params, B: int, T: int) -> int:

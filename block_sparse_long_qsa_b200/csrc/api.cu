@@ -1174,7 +1174,7 @@ qsa_status make_map_pages(CUtensorMap* m, const qsa_layer_params* p, const qsa::
   return QSA_OK;
 }
 
-void fill_rope(const qsa_layer_params* p, qsa::RopeSpec* r) {
+void make_rope(const qsa_layer_params* p, qsa::RopeSpec* r) {
   const int half = p->rope_dim / 2;
   r->half = half;
   r->eps = p->norm_eps;
@@ -1193,6 +1193,21 @@ void fill_rope(const qsa_layer_params* p, qsa::RopeSpec* r) {
     }
     r->axis[i] = (uint8_t)a;
   }
+}
+
+// make_rope's result for the parameters of this thread's last call, or anew: the
+// powers take as long as a launch.
+void fill_rope(const qsa_layer_params* p, qsa::RopeSpec* r) {
+  thread_local bool known = false;
+  thread_local qsa_layer_params last;
+  thread_local qsa::RopeSpec spec;
+  if (!known || std::memcmp(&last, p, sizeof(last)) != 0) {
+    std::memset(&spec, 0, sizeof(spec));
+    make_rope(p, &spec);
+    std::memcpy(&last, p, sizeof(last));
+    known = true;
+  }
+  *r = spec;
 }
 
 size_t paged_ws(const qsa_layer_params* p, int32_t B) {
