@@ -77,6 +77,13 @@ struct Visible {
   __device__ __forceinline__ int key(int v) const { return v < ns ? v : lo + (v - ns); }
 };
 
+// x / y for 0 <= x, 0 < y: in 32 bits where both fit (a 64-bit division is a
+// routine of about a hundred instructions).
+__device__ __forceinline__ int64_t div64(int64_t x, int64_t y) {
+  if (((uint64_t)(x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+  return x / y;
+}
+
 template <class E, int D>
 __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int WARPS = warps_of(D), THREADS = 32 * WARPS;
@@ -132,7 +139,10 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
   // CTAs that take part: no more than there are units, so none is without one
   const int n_cta = (int)min((int64_t)gridDim.x, total);
   const bool part = (int)blockIdx.x < n_cta;
-  const int64_t ua = part ? total * blockIdx.x / n_cta : 0, ub = part ? total * (blockIdx.x + 1) / n_cta : 0;
+  // CTA c has the units from c base + min(c, more) on: base, or one more
+  const int64_t base = part ? div64(total, n_cta) : 0, more = total - base * n_cta;
+  const int64_t ua = part ? base * blockIdx.x + min((int64_t)blockIdx.x, more) : 0;
+  const int64_t ub = part ? ua + base + ((int64_t)blockIdx.x < more ? 1 : 0) : 0;
   Scratch sc = scratch_of(a.scratch);
   if (tid == 0) sc.rec[blockIdx.x] = {0, 0, -1};
 
@@ -149,7 +159,7 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
     }
     const int nu = P[lo + 1] - P[lo];
     const int64_t r = x - (int64_t)P[lo] * HM;
-    const int hm = (int)(r / nu);
+    const int hm = (int)div64(r, nu);
     return {lo, hm, (int)(r - (int64_t)hm * nu), nu};
   };
   auto next_item = [&](At& p) {                   // first unit of the item after p's
@@ -186,6 +196,7 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
     ia = locate(ua);
     load_ids(true);
   }
+  At ca = ia;                                      // where the products are
   const uint32_t ring = smem_u32(smem) + warp * STAGES * SLOT;
   // strides in 16-byte units fit 32 bits (checked on the host)
   const uint32_t page16 = (uint32_t)(a.kv.page_stride >> 3), token16 = (uint32_t)(a.kv.token_stride >> 3);
@@ -251,8 +262,6 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
   // ---- products
   const uint32_t q_base = smem_u32(smem) + OFF_Q;
   int slot = 0;
-  At ca{0, 0, 0, 1};
-  if (ua < ub) ca = locate(ua);
   for (int64_t x = ua; x < ub;) {
     const int n_units = (int)min((int64_t)(ca.nu - ca.u), ub - x);
     const bool whole = n_units == ca.nu;
@@ -267,6 +276,13 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
       *reinterpret_cast<uint4*>(smem + OFF_Q + row_chunk<D>(r, c)) = v;
     }
     __syncthreads();
+    // up to 128 dims the queries stay in registers
+    constexpr bool QREG = D <= 128;
+    const uint32_t qr = (lane & 7) + ((lane >> 3) & 1) * 8;
+    uint32_t qf[QREG ? D / 16 : 1][4];
+    if (QREG)
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) ldsm4(qf[ks], q_base + row_chunk<D>(qr, 2 * ks + (lane >> 4)));
 
     float o[NO][4];
 #pragma unroll
@@ -289,11 +305,11 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
         for (int n = 0; n < CH * NK; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sp[n / NK][n % NK][e] = 0.f;
-        const uint32_t qr = (lane & 7) + ((lane >> 3) & 1) * 8, kr = (lane >> 4) * 8 + (lane & 7);
+        const uint32_t kr = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t qa[4];
-          ldsm4(qa, q_base + row_chunk<D>(qr, 2 * ks + (lane >> 4)));
+          uint32_t (&qa)[4] = qf[QREG ? ks : 0];
+          if (!QREG) ldsm4(qa, q_base + row_chunk<D>(qr, 2 * ks + (lane >> 4)));
 #pragma unroll
           for (int n = 0; n < NK; n += 2) {
             uint32_t kb[4];
@@ -433,7 +449,11 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
       }
     }
     if (!whole && item0 >= ua && tid == 0)
-      sc.rec[blockIdx.x] = {ca.b, ca.hm, (int32_t)(((item0 + ca.nu) * n_cta - 1) / total)};
+    {
+      const int64_t u = item0 + ca.nu - 1;         // the item's last unit, and the CTA that has it
+      const int64_t last = u < more * (base + 1) ? div64(u, base + 1) : more + div64(u - more * (base + 1), base);
+      sc.rec[blockIdx.x] = {ca.b, ca.hm, (int32_t)last};
+    }
     __syncthreads();
     issue();                                       // the merge's slot is free
     x += n_units;

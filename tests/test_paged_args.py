@@ -236,10 +236,14 @@ def test_decode_split_covers_every_unit_once():
             start[b, hm] = total
             total += u
         n_cta = min(G, total)
+        if total == 0:
+            continue
+        base, more = total // n_cta, total % n_cta
         pieces, rec, whole = {}, {}, set()
         for c in range(n_cta):
-            ua, ub = total * c // n_cta, total * (c + 1) // n_cta
-            assert ua < ub
+            ua = base * c + min(c, more)
+            ub = ua + base + (1 if c < more else 0)
+            assert ua < ub and (c or ua == 0) and (c < n_cta - 1 or ub == total)
             for b, hm, u in items:
                 s, e = start[b, hm], start[b, hm] + u
                 lo, hi = max(s, ua), min(e, ub)
@@ -253,7 +257,8 @@ def test_decode_split_covers_every_unit_once():
                 pieces[slot] = (b, hm, lo - s, hi - s)
                 if s >= ua:
                     assert c not in rec
-                    rec[c] = (b, hm, (e * n_cta - 1) // total)
+                    x = e - 1                       # the CTA of the item's last unit
+                    rec[c] = (b, hm, x // (base + 1) if x < more * (base + 1) else more + (x - more * (base + 1)) // base)
         for c, (b, hm, last) in rec.items():
             at = 0
             for i in range(last - c + 1):
