@@ -1383,16 +1383,18 @@ qsa_status qsa_paged_prefill(const qsa_layer_params* p, const qsa_paged_kv* kv, 
   a.err = static_cast<uint32_t*>(ws);
   a.scratch = static_cast<uint8_t*>(ws) + HEADER_BYTES;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  CUtensorMap tk{};
+  CUtensorMap tk{}, tv{};
   const int box = qsa::paged_prefill_box(a.kv.page_size);
-  if (box > 1 && (st = make_map_pages(&tk, p, a.kv, a.kv.k, box)) != QSA_OK) return st;
+  if (box > 1 && ((st = make_map_pages(&tk, p, a.kv, a.kv.k, box)) != QSA_OK ||
+                  (st = make_map_pages(&tv, p, a.kv, a.kv.v, box)) != QSA_OK))
+    return st;
   if ((st = from_cuda(traced(QSA_KERNEL_PAGED_PREFILL, s, [&] {
-         return qsa::launch_paged_prefill(a, tk, p->head_dim, p->dtype, di.num_sms, s, false);
+         return qsa::launch_paged_prefill(a, tk, tv, p->head_dim, p->dtype, di.num_sms, s, false);
        }), "paged prefill launch")) != QSA_OK)
     return st;
-  if (!qsa::paged_prefill_splits(a, di.num_sms)) return QSA_OK;
+  if (!qsa::paged_prefill_splits(a, p->head_dim, di.num_sms)) return QSA_OK;
   return from_cuda(traced(QSA_KERNEL_PAGED_PREFILL_JOIN, s, [&] {
-    return qsa::launch_paged_prefill(a, tk, p->head_dim, p->dtype, di.num_sms, s, true);
+    return qsa::launch_paged_prefill(a, tk, tv, p->head_dim, p->dtype, di.num_sms, s, true);
   }), "paged prefill join launch");
 }
 

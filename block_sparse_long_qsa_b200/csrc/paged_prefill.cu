@@ -39,215 +39,22 @@
 // n_split ranges so that the SMs fill up; the ranges' results go to the scratch
 // as normalised fp32 rows with their log-sum-exp, and the join kernel adds them
 // in the order of the keys.
-#include <cfloat>
-#include <type_traits>
-
-#include "paged.cuh"
+#include "paged_prefill.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int KT = 128;                             // keys of a tile
 constexpr int M = 128;                              // query rows of an item
-constexpr int W_LOAD = 8, LWARPS = 4, W_MMA = 12, W_TMA = 13, W_PV = 14;
-constexpr int LOADERS = 32 * LWARPS;
-constexpr int THREADS = 512;                        // warp 15 only makes up the last warpgroup
-constexpr int REGS_SOFT = 168, REGS_REST = 88;
-static_assert(256 * (REGS_SOFT + REGS_REST) <= 65536, "register split");
-constexpr int RT = LOADERS / 8, RJ = KT / RT;       // cp.async: rows of a pass, passes of a tile
+constexpr int64_t PAIR_ROWS = 512;                  // query rows of a sequence, on average, from which pairs are used
 constexpr uint32_t SLOT = 16384;
 constexpr int NS = 5;                               // slots of the K ring and of the V ring
 constexpr uint32_t OFF_K = 65536;                   // Q: up to 128 rows x 512 B
 constexpr uint32_t OFF_V = OFF_K + NS * SLOT;
 constexpr uint32_t OFF_XCH = OFF_V + NS * SLOT;     // running maxima [2][128], row sums [2][128]
 constexpr uint32_t OFF_OK = OFF_XCH + 2048;         // rows that are there, of NOK tiles, 32 bytes each
-// tiles whose row bits are live: K runs at most 6 tiles ahead of S (D = 64: the
-// ring holds 5), S 2 ahead of the softmax
-constexpr int NOK = 16;
 constexpr uint32_t OFF_BAR = OFF_OK + 32 * NOK;
 constexpr uint32_t SMEM = OFF_BAR + 384;
 static_assert(SMEM <= 232448, "prefill smem");
-constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t TM_S = 0, TM_O = 256;            // S / P buffers at 0 and 128
-constexpr int MAX_PIECES = 160;                     // bound of the scratch
-constexpr int MAX_SPLIT = 32;
-constexpr float RAISE = 8.f;                        // lazy maximum: P stays below 2^8
-
-__device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t c16) {
-  return row * 128u + ((c16 ^ (row & 7u)) << 4);
-}
-__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// mbar_wait with the thread suspended for up to 10 us at a time instead of
-// polling: sixteen warps that poll slow the others' shared-memory and
-// special-function instructions.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
-  uint64_t t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
-        : "memory");
-    if (ok) return true;
-    if (it == 0) t0 = globaltimer();
-    if (*abort_flag) return false;
-    if (globaltimer() - t0 > QSA_WAIT_TIMEOUT_NS) {
-      *abort_flag = 1;
-      report_error(err, QSA_ERR_DEVICE_TIMEOUT);
-      return false;
-    }
-  }
-}
-// The barrier's phase waits for this thread's copies so far, beside its counted
-// arrivals (this form adds the arrival that it makes to the pending count).
-__device__ __forceinline__ void cp_async_hold(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-// A box of a page: dims, rows of the page, KV head, page (no multicast).
-__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* m, int32_t dim, int32_t row, int32_t head,
-                                             int32_t page, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(dim), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
-      : "memory");
-}
-// Operand descriptors, 128-byte swizzle, as constant fields and a start address:
-// K-major (rows of 64 elements, 8-row groups 1024 bytes apart) and MN-major (lbo
-// bytes between 64-element atoms along N, 1024 between 8-row groups along K).
-constexpr uint64_t DESC_K = (uint64_t)1u << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
-__host__ __device__ constexpr uint64_t desc_mn(uint32_t lbo) {
-  return (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
-}
-__device__ __forceinline__ uint64_t desc_at(uint64_t fields, uint32_t addr) { return fields | (addr >> 4); }
-// The MMA warp stays converged and one elected lane issues (always the same one):
-// descriptors and addresses then live in uniform registers.  Inside a one-lane
-// branch each MMA first moves them there, which took longer than the MMA.
-// D[tmem] (+)= A[smem] * B[smem]^T
-__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-      ::"r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-struct Grid {
-  int64_t n_slots;          // tile slots of the batch
-  int n_split;
-};
-struct Scratch {
-  float* lse2;              // [MAX_PIECES][128]
-  float* o;                 // [MAX_PIECES][128][D]
-};
-__host__ __device__ inline Scratch scratch_of(void* p) {
-  return {static_cast<float*>(p), static_cast<float*>(p) + MAX_PIECES * M};
-}
-
-struct Args {
-  CUtensorMap tk;           // K pages, boxes of `box` rows x 64 dims
-  PagedAttnArgs a;
-  Grid grid;
-  int box;                  // 16, 32 or 64, or 1: no TMA
-};
-
-// Item w.  Sequence b owns the tile slots from cu[b] per / 128 + b on (at least
-// as many as it has tiles), so a slot's sequence is found by bisection and the
-// slots without a tile are items without keys.
-struct Item {
-  int b, g, rows;           // sequence, KV head, rows in use
-  int n_tiles, tile0;       // tiles of this range, its first
-  int pieces, split;        // ranges that the item's keys are cut into, which one this is
-  int lo, ns, n_vis;        // key number v: v < ns ? v : lo + v - ns (whole boxes)
-  int first, end;           // keys needed: [first, end) and those below the sinks
-  int p0;                   // position of the first row's token
-  int64_t t0, row0;         // the sequence's first token row; first flat row of the item
-  __device__ __forceinline__ Item(const Args& x, int64_t w) {
-    const PagedAttnArgs& a = x.a;
-    const int per = a.hq / a.hk, ns_ = x.grid.n_split;
-    n_tiles = 0;
-    tile0 = 0;
-    split = (int)(w % ns_);
-    w /= ns_;
-    g = (int)(w % a.hk);
-    const int64_t slot = x.grid.n_slots - 1 - w / a.hk;
-    int l = 0, h = a.B;
-    while (h - l > 1) {
-      const int mid = (l + h) >> 1;
-      if ((int64_t)__ldg(a.cu_new + mid) * per / M + mid <= slot) l = mid; else h = mid;
-    }
-    b = l;
-    t0 = __ldg(a.cu_new + b);
-    const int64_t t1 = min((int64_t)__ldg(a.cu_new + b + 1), a.T);
-    const int L = __ldg(a.cache_len + b);
-    const int64_t tile = slot - (t0 * per / M + b), n_rows = (t1 - t0) * per;
-    row0 = tile * M;
-    rows = (int)min((int64_t)M, n_rows - row0);
-    if (t0 < 0 || tile < 0 || rows <= 0 || L < 0) return;
-    const int64_t pos = L + row0 / per, last = L + (row0 + rows - 1) / per;
-    end = (int)min(last + 1, (int64_t)a.kv.capacity);
-    if (last >= a.kv.capacity) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
-    first = a.window > 0 && pos >= a.window ? (int)min(pos - a.window + 1, (int64_t)end) : 0;
-    lo = first / x.box * x.box;
-    ns = min((a.sinks + x.box - 1) / x.box * x.box, lo);
-    if (ns == lo) ns = lo = 0;                      // no gap
-    n_vis = ns + end - lo;
-    p0 = (int)min(pos, (int64_t)INT32_MAX);
-    // at least one tile: rows whose keys all lie past the table come out zero
-    const int all = max((n_vis + KT - 1) / KT, 1), each = (all + ns_ - 1) / ns_;
-    pieces = (all + each - 1) / each;
-    tile0 = split * each;
-    n_tiles = min(each, all - tile0);
-  }
-};
 
 template <class E, int D, bool TMA>
 __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_constant__ Args x) {
@@ -324,7 +131,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       if (lane == 0) mbar_arrive(bar);
     };
     for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
-      const Item it(x, w);
+      const Item<M> it(x, w);
       if (it.n_tiles <= 0) continue;
       const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
       const int64_t head = (int64_t)it.g * a.kv.head_stride + 8 * c;
@@ -451,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     bool ok = true;
     const int box = x.box, nb = KT / box;
     for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
-      const Item it(x, w);
+      const Item<M> it(x, w);
       if (it.n_tiles <= 0) continue;
       const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
       // lane i has box i of a tile (lanes past the last repeat): its page, or -1
@@ -514,7 +321,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
     };
     for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
-      const Item it(x, w);
+      const Item<M> it(x, w);
       const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
       if (n_tiles <= 0) continue;
       if (!wait(q_full, items_done & 1)) { ok = false; break; }
@@ -560,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
     };
     for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
-      const Item it(x, w);
+      const Item<M> it(x, w);
       const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
       if (n_tiles <= 0) continue;
       if (items_done > 0 && !wait(o_empty, (items_done - 1) & 1)) { ok = false; break; }
@@ -593,192 +400,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   } else if (warp < W_LOAD) {
     // ---------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
-    const int quad = warp & 3, wg = warp >> 2;      // rows 32 quad .., tiles with count % 2 == wg
-    const int r = 32 * quad + lane;
-    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-    volatile float* m_pub = reinterpret_cast<volatile float*>(smem + OFF_XCH);      // [2][128]
-    volatile float* l_pub = m_pub + 2 * M;                                          // [2][128]
-    uint32_t count = 0, items_done = 0;             // count: tiles of the items before
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
-    };
-    for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
-      int n_tiles, v0;                                // tiles of the item, first key number of the tile
-      int v_min, v_max;                               // the row sees v in [v_min, v_max] and v < sinks
-      int all_min, all_max;                           // every row sees v in [all_min, all_max]
-      int64_t orow;                                   // output row, or piece row; -1: row not in use
-      bool part;
-      {
-        const Item it(x, w);
-        if (it.n_tiles <= 0) continue;
-        n_tiles = it.n_tiles;
-        v0 = it.tile0 * KT;
-        const bool in = r < it.rows;
-        const int64_t flat = it.row0 + (in ? r : 0), tok0 = it.row0 / per;
-        const int shift = it.ns - it.lo;              // position -> number, behind the gap
-        const int64_t pos = (int64_t)it.p0 + (flat / per - tok0);
-        const int64_t pos1 = (int64_t)it.p0 + ((it.row0 + it.rows - 1) / per - tok0);
-        v_max = (int)min(pos + shift, (int64_t)it.n_vis - 1);
-        all_max = (int)min((int64_t)it.p0 + shift, (int64_t)it.n_vis - 1);
-        v_min = a.window > 0 ? (int)max(pos - a.window + 1 + shift, (int64_t)0) : 0;
-        all_min = a.window > 0 ? (int)max(pos1 - a.window + 1 + shift, (int64_t)0) : 0;
-        part = it.pieces > 1;
-        orow = !in ? -1 : part ? w * M + r : (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
-      }
-      float m = -FLT_MAX, l = 0.f;
-      for (int i = (int)((count ^ wg) & 1); i < n_tiles; i += 2) {
-        const uint32_t n = count + i, buf = wg;     // n % 2 == wg
-        if (!wait(&s_full[buf], (n >> 1) & 1)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t s_addr = tmem + lanes + TM_S + 128 * buf;
-        float s[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, s[q]);
-        // the keys that are there, four to a byte
-        const uint4* there = reinterpret_cast<const uint4*>(smem + OFF_OK + (n % NOK) * 32);
-        const uint4 t0 = there[0], t1 = there[1];
-        const int vt = v0 + i * KT;
-        const bool whole = vt + KT - 1 <= all_max && (vt >= all_min || vt + KT <= a.sinks) &&
-                           (t0.x & t0.y & t0.z & t0.w & t1.x & t1.y & t1.z & t1.w) == 0x0f0f0f0fu;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld_wait(s[q]);
-        if (!whole) {
-          const uint32_t bits[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
-          auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-          auto squeeze = [](uint32_t x) -> uint32_t {   // four bits of each byte to 16
-            x = (x | x >> 4) & 0x00ff00ffu;
-            return (x | x >> 8) & 0xffffu;
-          };
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int vq = vt + 32 * q;
-            const uint32_t mask = (squeeze(bits[2 * q]) | squeeze(bits[2 * q + 1]) << 16) & below(v_max + 1 - vq) &
-                                  (~below(v_min - vq) | below(a.sinks - vq));
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(mask >> e & 1)) s[q][e] = -INFINITY;
-          }
-        }
-        float mt = -INFINITY, mu = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          mt = max3f(mt, s[0][e], s[1][e]);
-          mu = max3f(mu, s[2][e], s[3][e]);
-        }
-        mt = fmaxf(fmaxf(mt, mu) * a.scale_log2, -FLT_MAX);   // a tile without a key leaves the maximum as it is
-        // the maximum after the tile before, from the other group (also between
-        // items, where it is not used, so that no barrier runs two phases ahead)
-        if (n > 0) {
-          if (!wait(&hand[(wg ^ 1) * 4 + quad], ((n - 1) >> 1) & 1)) { ok = false; break; }
-        }
-        if (i > 0) {
-          const float mp = m_pub[(wg ^ 1) * M + r];
-          l *= exp2_approx(m - mp);
-          m = mp;
-        }
-        const bool raise = mt > m + RAISE;
-        const float m_old = m;
-        if (raise) m = mt;
-        m_pub[wg * M + r] = m;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&hand[wg * 4 + quad]);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float f = exp2_approx(m_old - m);
-          l *= f;
-          if (i > 0) {
-            // O holds the tiles up to i - 1 once their P V is done; this tile's
-            // waits for this warp
-            if (!wait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
-            tc_fence_after();
-#pragma unroll 1
-            for (int cc = 0; cc < D / 16; ++cc) {
-              uint32_t o[16];
-              const uint32_t ad = tmem + lanes + TM_O + 16 * cc;
-              tmem_ld16(ad, o);                     // waits for the load
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(ad, o);
-            }
-          }
-        }
-        // p = 2^(s scale - m); the sum takes the fp32 values, the products p
-        // rounded to 16 bits.  P takes the first half of the scores' columns.
-        const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-m, -m);
-        uint64_t sum = pk2(0.f, 0.f);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float x0, x1;
-            upk2(fma2(pk2(s[q][2 * e], s[q][2 * e + 1]), sc2, nm2), x0, x1);
-            x0 = exp2_approx(x0);
-            x1 = exp2_approx(x1);
-            sum = add2(sum, pk2(x0, x1));
-            pk[e] = X::pack(x0, x1);
-          }
-          tmem_st16(s_addr + 16 * q, pk);
-        }
-        float l0, l1;
-        upk2(sum, l0, l1);
-        l += l0 + l1;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[buf]);
-      }
-      if (!ok) break;
-      // ---- O / l
-      count += n_tiles;
-      const uint32_t n = count - 1;                 // the item's last tile
-      if ((n & 1) != (uint32_t)wg) {                // the other group's: its maximum is the last
-        if (!wait(&hand[(wg ^ 1) * 4 + quad], (n >> 1) & 1)) { ok = false; break; }
-        const float mp = m_pub[(wg ^ 1) * M + r];
-        l *= exp2_approx(m - mp);
-        m = mp;
-      }
-      // (this P V began after both groups had taken the item before's sums)
-      if (!wait(&pv_done[n & 1], (n >> 1) & 1)) { ok = false; break; }
-      tc_fence_after();
-      l_pub[wg * M + r] = l;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&xbar[quad]);
-      if (!wait(&xbar[quad], items_done & 1)) { ok = false; break; }
-      const float l_other = l_pub[(wg ^ 1) * M + r];
-      const float lr = l + l_other;
-      const float inv = lr == 0.f ? 0.f : 1.f / lr;   // no key at all: zero
-      const float lse2 = lr == 0.f ? -INFINITY : m + log2f(lr);
-      const Scratch sc = scratch_of(a.scratch);
-#pragma unroll 1
-      for (int cc = 0; cc < D / 64; ++cc) {
-        float o[32];
-        const int d0 = (D / 2) * wg + 32 * cc;
-        tmem_ld32(tmem + lanes + TM_O + d0, o);
-        tmem_ld_wait(o);
-        if (orow >= 0 && part) {
-          float4* dst = reinterpret_cast<float4*>(sc.o + orow * D + d0);
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[q] = make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv, o[4 * q + 3] * inv);
-        } else if (orow >= 0) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + d0);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            dst[q] = make_uint4(X::pack(o[8 * q] * inv, o[8 * q + 1] * inv), X::pack(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
-                                X::pack(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
-                                X::pack(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
-        }
-      }
-      if (orow >= 0 && wg == 0) {
-        if (part) sc.lse2[orow] = lse2;
-        else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_empty);
-      ++items_done;
-    }
+    softmax_role<E, D, M, false>(x, smem, OFF_OK, OFF_XCH, {s_full, nullptr, p_full, pv_done, hand, xbar, o_empty}, tmem, warp,
+                                 lane, 0, blockIdx.x, gridDim.x, n_items, abort_flag);
   }
   tc_fence_before();
   __syncthreads();
@@ -789,7 +412,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
 }
 
 // Joins the ranges of items whose keys were cut: one warp a query row.
-template <class E, int D>
+template <class E, int D, int M>
 __global__ void __launch_bounds__(256) paged_prefill_join_kernel(const __grid_constant__ Args x) {
   constexpr int W = D / 32;                         // dims of a lane: 2, 4 or 8
   using X = Elem<E>;
@@ -799,7 +422,7 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(const __grid_co
   const int64_t w0 = id / M * x.grid.n_split;       // the item's first range
   const int r = (int)(id % M), lane = threadIdx.x & 31;
   if (w0 >= x.grid.n_slots * a.hk * x.grid.n_split) return;
-  const Item it(x, w0);
+  const Item<M> it(x, w0);
   if (it.n_tiles <= 0 || it.pieces <= 1 || r >= it.rows) return;
   const Scratch sc = scratch_of(a.scratch);
   float m = -FLT_MAX, l = 0.f, acc[W];
@@ -827,12 +450,21 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(const __grid_co
   if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-Grid grid_of(const PagedAttnArgs& a, int num_sms) {
+// Whether pairs of CTAs take the batch (paged_prefill_pair.cu): head dim 256,
+// pages that TMA can fetch, and sequences that fill tiles of 256 rows on average.
+bool use_pair(const PagedAttnArgs& a, int head_dim) {
+  return head_dim == 256 && paged_prefill_box(a.kv.page_size) > 1 && a.T * (a.hq / a.hk) >= PAIR_ROWS * a.B;
+}
+
+Grid grid_of(const PagedAttnArgs& a, int head_dim, int num_sms) {
+  const bool pair = use_pair(a, head_dim);
+  const int m = pair ? 256 : 128;
   Grid g;
-  g.n_slots = (a.T * (a.hq / a.hk) + M - 1) / M + a.B;
+  g.n_slots = (a.T * (a.hq / a.hk) + m - 1) / m + a.B;
   // ranges: as many as fill the SMs, from the slots (a sequence's last slot is
   // often empty, so the SMs are filled to about a half at the least)
-  const int64_t n = (num_sms < MAX_PIECES ? num_sms : MAX_PIECES) / (g.n_slots * a.hk);
+  const int sms = num_sms < MAX_PIECES ? num_sms : MAX_PIECES;
+  const int64_t n = (pair ? sms / 2 : sms) / (g.n_slots * a.hk);
   g.n_split = (int)(n < 1 ? 1 : (n > MAX_SPLIT ? MAX_SPLIT : n));
   return g;
 }
@@ -852,20 +484,10 @@ cudaError_t launch_attn(const Args& x, int grid, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <class E, int D>
-cudaError_t launch_d(const PagedAttnArgs& a, const CUtensorMap& tk, int num_sms, cudaStream_t s, bool join) {
-  Args x;
-  x.tk = tk;
-  x.a = a;
-  x.grid = grid_of(a, num_sms);
-  x.box = paged_prefill_box(a.kv.page_size);
-  const int64_t items = x.grid.n_slots * a.hk * x.grid.n_split;
-  if (!join) {
-    const int grid = (int)(items < num_sms ? items : num_sms);
-    return x.box > 1 ? launch_attn<E, D, true>(x, grid, s) : launch_attn<E, D, false>(x, grid, s);
-  }
+template <class E, int D, int M>
+cudaError_t launch_join(const Args& x, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items / x.grid.n_split * (M / 8)));
+  cfg.gridDim = dim3((unsigned)(x.grid.n_slots * x.a.hk * (M / 8)));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -873,21 +495,46 @@ cudaError_t launch_d(const PagedAttnArgs& a, const CUtensorMap& tk, int num_sms,
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<E, D>, x);
+  return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<E, D, M>, x);
+}
+
+template <class E, int D>
+cudaError_t launch_d(const PagedAttnArgs& a, const CUtensorMap& tk, int num_sms, cudaStream_t s, bool join) {
+  Args x;
+  x.tk = tk;
+  x.tv = tk;
+  x.a = a;
+  x.grid = grid_of(a, D, num_sms);
+  x.box = paged_prefill_box(a.kv.page_size);
+  if (join) {
+    if constexpr (D == 256)
+      if (use_pair(a, D)) return launch_join<E, D, 256>(x, s);
+    return launch_join<E, D, 128>(x, s);
+  }
+  const int64_t items = x.grid.n_slots * a.hk * x.grid.n_split;
+  const int grid = (int)(items < num_sms ? items : num_sms);
+  return x.box > 1 ? launch_attn<E, D, true>(x, grid, s) : launch_attn<E, D, false>(x, grid, s);
 }
 
 }  // namespace
 
 size_t paged_prefill_scratch(int head_dim) { return (size_t)MAX_PIECES * M * (head_dim + 1) * 4; }
 
-bool paged_prefill_splits(const PagedAttnArgs& a, int num_sms) { return grid_of(a, num_sms).n_split > 1; }
+bool paged_prefill_splits(const PagedAttnArgs& a, int head_dim, int num_sms) {
+  return grid_of(a, head_dim, num_sms).n_split > 1;
+}
 
 int paged_prefill_box(int page_size) {
   return page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : page_size % 16 == 0 ? 16 : 1;
 }
 
-cudaError_t launch_paged_prefill(const PagedAttnArgs& a, const CUtensorMap& tk, int head_dim, int dtype, int num_sms, cudaStream_t s, bool join) {
+cudaError_t launch_paged_prefill(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
+                                 int dtype, int num_sms, cudaStream_t s, bool join) {
   if (a.B <= 0 || a.T <= 0) return cudaSuccess;
+  if (!join && use_pair(a, head_dim)) {
+    const Grid g = grid_of(a, head_dim, num_sms);
+    return launch_paged_prefill_pair(a, tk, tv, dtype, g.n_slots, g.n_split, num_sms, s);
+  }
   const bool bf = dtype == QSA_DTYPE_BF16;
   switch (head_dim) {
     case 64: return bf ? launch_d<__nv_bfloat16, 64>(a, tk, num_sms, s, join)

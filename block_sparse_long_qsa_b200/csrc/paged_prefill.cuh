@@ -1,0 +1,473 @@
+// What the two prefill kernels share: waits, TMA and tcgen05 instructions, the
+// items of a ragged batch, and the softmax warps.
+#pragma once
+#include <cfloat>
+#include <type_traits>
+
+#include "paged.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int KT = 128;                             // keys of a tile
+constexpr int THREADS = 512;
+constexpr int REGS_SOFT = 168, REGS_REST = 88;
+static_assert(256 * (REGS_SOFT + REGS_REST) <= 65536, "register split");
+constexpr int W_LOAD = 8, LWARPS = 4, W_MMA = 12, W_TMA = 13, W_PV = 14;   // warp 15 only makes up the warpgroup
+constexpr int LOADERS = 32 * LWARPS;
+constexpr int RT = LOADERS / 8, RJ = KT / RT;       // cp.async: rows of a pass, passes of a tile
+// tiles whose row bits are live: K runs at most 6 tiles ahead of S (D = 64: the
+// ring holds 5), S 2 ahead of the softmax
+constexpr int NOK = 16;
+constexpr uint32_t TMEM_COLS = 512;
+// One CTA: S / P buffers at columns 0 and 128.  Pair: S at 0, P at 128 and 192.
+constexpr uint32_t TM_S = 0, TM_P = 128, TM_O = 256;
+constexpr int MAX_PIECES = 160;                     // bound of the scratch, pieces of 128 rows
+constexpr int MAX_SPLIT = 32;
+constexpr float RAISE = 8.f;                        // lazy maximum: P stays below 2^8
+
+__device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t c16) {
+  return row * 128u + ((c16 ^ (row & 7u)) << 4);
+}
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// mbar_wait with the thread suspended for up to 10 us at a time instead of
+// polling: sixteen warps that poll slow the others' shared-memory and
+// special-function instructions.
+// CLUSTER: the arrivals may come from the other CTA of a pair.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t ok;
+    if (CLUSTER)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+          : "memory");
+    if (ok) return true;
+    if (it == 0) t0 = globaltimer();
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > QSA_WAIT_TIMEOUT_NS) {
+      *abort_flag = 1;
+      report_error(err, QSA_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+  }
+}
+// One arrival on the same barrier of the pair's first CTA.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+}
+// The barrier's phase waits for this thread's copies so far, beside its counted
+// arrivals (this form adds the arrival that it makes to the pending count).
+__device__ __forceinline__ void cp_async_hold(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// A box of a page: dims, rows of the page, KV head, page (no multicast).
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* m, int32_t dim, int32_t row, int32_t head,
+                                             int32_t page, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(dim), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+// Operand descriptors, 128-byte swizzle, as constant fields and a start address:
+// K-major (rows of 64 elements, 8-row groups 1024 bytes apart) and MN-major (lbo
+// bytes between 64-element atoms along N, 1024 between 8-row groups along K).
+constexpr uint64_t DESC_K = (uint64_t)1u << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
+__host__ __device__ constexpr uint64_t desc_mn(uint32_t lbo) {
+  return (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+__device__ __forceinline__ uint64_t desc_at(uint64_t fields, uint32_t addr) { return fields | (addr >> 4); }
+// The MMA warp stays converged and one elected lane issues (always the same one):
+// descriptors and addresses then live in uniform registers.  Inside a one-lane
+// branch each MMA first moves them there, which took longer than the MMA.
+// GROUP 2: one MMA over the pair's two CTAs, issued by the first: each holds half
+// of A's rows (and of D's) and half of B's columns, at the same addresses.
+// D[tmem] (+)= A[smem] * B[smem]^T
+template <int GROUP = 1>
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  if (GROUP == 1)
+    asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+  else
+    asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+template <int GROUP = 1>
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  if (GROUP == 1)
+    asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+  else
+    asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+template <int GROUP = 1>
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+  if (GROUP == 1)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(smem_u32(bar))
+        : "memory");
+  else   // on the same barrier of both CTAs
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+        ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+struct Grid {
+  int64_t n_slots;          // tile slots of the batch
+  int n_split;
+};
+struct Scratch {
+  float* lse2;              // [MAX_PIECES][128]
+  float* o;                 // [MAX_PIECES][128][D]
+};
+__host__ __device__ inline Scratch scratch_of(void* p) {
+  return {static_cast<float*>(p), static_cast<float*>(p) + MAX_PIECES * 128};
+}
+
+struct Args {
+  CUtensorMap tk, tv;       // pages, boxes of `box` rows x 64 dims (tv: the pair kernel's)
+  PagedAttnArgs a;
+  Grid grid;
+  int box;                  // 16, 32 or 64, or 1: no TMA
+};
+
+// Item w of M query rows.  Sequence b owns the tile slots from cu[b] per / M + b on (at least
+// as many as it has tiles), so a slot's sequence is found by bisection and the
+// slots without a tile are items without keys.
+template <int M>
+struct Item {
+  int b, g, rows;           // sequence, KV head, rows in use
+  int n_tiles, tile0;       // tiles of this range, its first
+  int pieces, split;        // ranges that the item's keys are cut into, which one this is
+  int lo, ns, n_vis;        // key number v: v < ns ? v : lo + v - ns (whole boxes)
+  int first, end;           // keys needed: [first, end) and those below the sinks
+  int p0;                   // position of the first row's token
+  int64_t t0, row0;         // the sequence's first token row; first flat row of the item
+  __device__ __forceinline__ Item(const Args& x, int64_t w) {
+    const PagedAttnArgs& a = x.a;
+    const int per = a.hq / a.hk, ns_ = x.grid.n_split;
+    n_tiles = 0;
+    tile0 = 0;
+    split = (int)(w % ns_);
+    w /= ns_;
+    g = (int)(w % a.hk);
+    const int64_t slot = x.grid.n_slots - 1 - w / a.hk;
+    int l = 0, h = a.B;
+    while (h - l > 1) {
+      const int mid = (l + h) >> 1;
+      if ((int64_t)__ldg(a.cu_new + mid) * per / M + mid <= slot) l = mid; else h = mid;
+    }
+    b = l;
+    t0 = __ldg(a.cu_new + b);
+    const int64_t t1 = min((int64_t)__ldg(a.cu_new + b + 1), a.T);
+    const int L = __ldg(a.cache_len + b);
+    const int64_t tile = slot - (t0 * per / M + b), n_rows = (t1 - t0) * per;
+    row0 = tile * M;
+    rows = (int)min((int64_t)M, n_rows - row0);
+    if (t0 < 0 || tile < 0 || rows <= 0 || L < 0) return;
+    const int64_t pos = L + row0 / per, last = L + (row0 + rows - 1) / per;
+    end = (int)min(last + 1, (int64_t)a.kv.capacity);
+    if (last >= a.kv.capacity) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
+    first = a.window > 0 && pos >= a.window ? (int)min(pos - a.window + 1, (int64_t)end) : 0;
+    lo = first / x.box * x.box;
+    ns = min((a.sinks + x.box - 1) / x.box * x.box, lo);
+    if (ns == lo) ns = lo = 0;                      // no gap
+    n_vis = ns + end - lo;
+    p0 = (int)min(pos, (int64_t)INT32_MAX);
+    // at least one tile: rows whose keys all lie past the table come out zero
+    const int all = max((n_vis + KT - 1) / KT, 1), each = (all + ns_ - 1) / ns_;
+    pieces = (all + each - 1) / each;
+    tile0 = split * each;
+    n_tiles = min(each, all - tile0);
+  }
+};
+
+// The softmax warps (0-7): row r0 + r of an item of ROWS rows in TMEM lane r, items
+// w0, w0 + w_step, ..  In a pair of CTAs (PAIR) S has one buffer, which is free as
+// soon as the scores are in registers, P has two of its own, and the MMA's
+// barriers are the first CTA's.
+struct SoftBars {
+  uint64_t *s_full, *s_empty, *p_full, *pv_done, *hand, *xbar, *o_empty;
+};
+template <class E, int D, int ROWS, bool PAIR>
+__device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint32_t off_ok, uint32_t off_xch, const SoftBars& bar,
+                                             uint32_t tmem, int warp, int lane, int r0, int64_t w0, int64_t w_step,
+                                             int64_t n_items, volatile int* abort_flag) {
+  using X = Elem<E>;
+  const PagedAttnArgs& a = x.a;
+  const int per = a.hq / a.hk;
+  const int quad = warp & 3, wg = warp >> 2;      // rows 32 quad .., tiles with count % 2 == wg
+  const int r = 32 * quad + lane;
+  const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+  volatile float* m_pub = reinterpret_cast<volatile float*>(smem + off_xch);      // [2][128]
+  volatile float* l_pub = m_pub + 2 * 128;                                          // [2][128]
+  uint32_t count = 0, items_done = 0;             // count: tiles of the items before
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, bar_wait<PAIR>(bar, parity, abort_flag, a.err));
+  };
+  for (int64_t w = w0; ok && w < n_items; w += w_step) {
+    int n_tiles, v0;                                // tiles of the item, first key number of the tile
+    int v_min, v_max;                               // the row sees v in [v_min, v_max] and v < sinks
+    int all_min, all_max;                           // every row sees v in [all_min, all_max]
+    int64_t orow;                                   // output row, or piece row; -1: row not in use
+    bool part;
+    {
+      const Item<ROWS> it(x, w);
+      if (it.n_tiles <= 0) continue;
+      n_tiles = it.n_tiles;
+      v0 = it.tile0 * KT;
+      const bool in = r0 + r < it.rows;
+      const int64_t flat = it.row0 + (in ? r0 + r : 0), tok0 = it.row0 / per;
+      const int shift = it.ns - it.lo;              // position -> number, behind the gap
+      const int64_t pos = (int64_t)it.p0 + (flat / per - tok0);
+      const int64_t pos1 = (int64_t)it.p0 + ((it.row0 + min(it.rows, r0 + 128) - 1) / per - tok0);
+      const int64_t pos_f = (int64_t)it.p0 + ((it.row0 + min(r0, it.rows - 1)) / per - tok0);
+      v_max = (int)min(pos + shift, (int64_t)it.n_vis - 1);
+      all_max = (int)min(pos_f + shift, (int64_t)it.n_vis - 1);
+      v_min = a.window > 0 ? (int)max(pos - a.window + 1 + shift, (int64_t)0) : 0;
+      all_min = a.window > 0 ? (int)max(pos1 - a.window + 1 + shift, (int64_t)0) : 0;
+      part = it.pieces > 1;
+      orow = !in ? -1 : part ? w * ROWS + r0 + r : (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
+    }
+    float m = -FLT_MAX, l = 0.f;
+    for (int i = (int)((count ^ wg) & 1); i < n_tiles; i += 2) {
+      const uint32_t n = count + i, buf = wg;     // n % 2 == wg
+      if (!wait(&bar.s_full[buf], (n >> 1) & 1)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t s_addr = tmem + lanes + TM_S + (PAIR ? 0 : 128 * buf);
+      const uint32_t p_addr = tmem + lanes + (PAIR ? TM_P + 64 * buf : TM_S + 128 * buf);
+      float s[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, s[q]);
+      // the keys that are there, four to a byte
+      const uint4* there = reinterpret_cast<const uint4*>(smem + off_ok + (n % NOK) * 32);
+      const uint4 t0 = there[0], t1 = there[1];
+      const int vt = v0 + i * KT;
+      const bool whole = vt + KT - 1 <= all_max && (vt >= all_min || vt + KT <= a.sinks) &&
+                         (t0.x & t0.y & t0.z & t0.w & t1.x & t1.y & t1.z & t1.w) == 0x0f0f0f0fu;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld_wait(s[q]);
+      if (PAIR) {                                 // the next S may overwrite these
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(bar.s_empty);
+      }
+      if (!whole) {
+        const uint32_t bits[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+        auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+        auto squeeze = [](uint32_t x) -> uint32_t {   // four bits of each byte to 16
+          x = (x | x >> 4) & 0x00ff00ffu;
+          return (x | x >> 8) & 0xffffu;
+        };
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int vq = vt + 32 * q;
+          const uint32_t mask = (squeeze(bits[2 * q]) | squeeze(bits[2 * q + 1]) << 16) & below(v_max + 1 - vq) &
+                                (~below(v_min - vq) | below(a.sinks - vq));
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(mask >> e & 1)) s[q][e] = -INFINITY;
+        }
+      }
+      float mt = -INFINITY, mu = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        mt = max3f(mt, s[0][e], s[1][e]);
+        mu = max3f(mu, s[2][e], s[3][e]);
+      }
+      mt = fmaxf(fmaxf(mt, mu) * a.scale_log2, -FLT_MAX);   // a tile without a key leaves the maximum as it is
+      // the maximum after the tile before, from the other group (also between
+      // items, where it is not used, so that no barrier runs two phases ahead)
+      if (n > 0) {
+        if (!wait(&bar.hand[(wg ^ 1) * 4 + quad], ((n - 1) >> 1) & 1)) { ok = false; break; }
+      }
+      if (i > 0) {
+        const float mp = m_pub[(wg ^ 1) * 128 + r];
+        l *= exp2_approx(m - mp);
+        m = mp;
+      }
+      const bool raise = mt > m + RAISE;
+      const float m_old = m;
+      if (raise) m = mt;
+      m_pub[wg * 128 + r] = m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.hand[wg * 4 + quad]);
+      if (__any_sync(0xffffffffu, raise)) {
+        const float f = exp2_approx(m_old - m);
+        l *= f;
+        if (i > 0) {
+          // O holds the tiles up to i - 1 once their P V is done; this tile's
+          // waits for this warp
+          if (!wait(&bar.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < D / 16; ++cc) {
+            uint32_t o[16];
+            const uint32_t ad = tmem + lanes + TM_O + 16 * cc;
+            tmem_ld16(ad, o);                     // waits for the load
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(ad, o);
+          }
+        }
+      }
+      // the P of two tiles before has been used (where P shares the scores'
+      // columns, this tile's S came after that)
+      if (PAIR && n >= 2 && !wait(&bar.pv_done[buf], ((n >> 1) - 1) & 1)) { ok = false; break; }
+      // p = 2^(s scale - m); the sum takes the fp32 values, the products p
+      // rounded to 16 bits
+      const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-m, -m);
+      uint64_t sum = pk2(0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float x0, x1;
+          upk2(fma2(pk2(s[q][2 * e], s[q][2 * e + 1]), sc2, nm2), x0, x1);
+          x0 = exp2_approx(x0);
+          x1 = exp2_approx(x1);
+          sum = add2(sum, pk2(x0, x1));
+          pk[e] = X::pack(x0, x1);
+        }
+        tmem_st16(p_addr + 16 * q, pk);
+      }
+      float l0, l1;
+      upk2(sum, l0, l1);
+      l += l0 + l1;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) arrive_leader(&bar.p_full[buf]);
+        else mbar_arrive(&bar.p_full[buf]);
+      }
+    }
+    if (!ok) break;
+    // ---- O / l
+    count += n_tiles;
+    const uint32_t n = count - 1;                 // the item's last tile
+    if ((n & 1) != (uint32_t)wg) {                // the other group's: its maximum is the last
+      if (!wait(&bar.hand[(wg ^ 1) * 4 + quad], (n >> 1) & 1)) { ok = false; break; }
+      const float mp = m_pub[(wg ^ 1) * 128 + r];
+      l *= exp2_approx(m - mp);
+      m = mp;
+    }
+    // (this P V began after both groups had taken the item before's sums)
+    if (!wait(&bar.pv_done[n & 1], (n >> 1) & 1)) { ok = false; break; }
+    tc_fence_after();
+    l_pub[wg * 128 + r] = l;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.xbar[quad]);
+    if (!wait(&bar.xbar[quad], items_done & 1)) { ok = false; break; }
+    const float l_other = l_pub[(wg ^ 1) * 128 + r];
+    const float lr = l + l_other;
+    const float inv = lr == 0.f ? 0.f : 1.f / lr;   // no key at all: zero
+    const float lse2 = lr == 0.f ? -INFINITY : m + log2f(lr);
+    const Scratch sc = scratch_of(a.scratch);
+#pragma unroll 1
+    for (int cc = 0; cc < D / 64; ++cc) {
+      float o[32];
+      const int d0 = (D / 2) * wg + 32 * cc;
+      tmem_ld32(tmem + lanes + TM_O + d0, o);
+      tmem_ld_wait(o);
+      if (orow >= 0 && part) {
+        float4* dst = reinterpret_cast<float4*>(sc.o + orow * D + d0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          dst[q] = make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv, o[4 * q + 3] * inv);
+      } else if (orow >= 0) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + d0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          dst[q] = make_uint4(X::pack(o[8 * q] * inv, o[8 * q + 1] * inv), X::pack(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                              X::pack(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
+                              X::pack(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+      }
+    }
+    if (orow >= 0 && wg == 0) {
+      if (part) sc.lse2[orow] = lse2;
+      else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if (PAIR) arrive_leader(bar.o_empty);
+      else mbar_arrive(bar.o_empty);
+    }
+    ++items_done;
+  }
+}
+
+}  // namespace
+}  // namespace qsa

@@ -180,12 +180,14 @@ size_t paged_decode_scratch(int head_dim, int B);
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, int head_dim, int dtype, int num_sms, cudaStream_t s,
                                 bool join);
 size_t paged_prefill_scratch(int head_dim);
-bool paged_prefill_splits(const PagedAttnArgs& a, int num_sms);   // whether the join is due
+bool paged_prefill_splits(const PagedAttnArgs& a, int head_dim, int num_sms);   // whether the join is due
 // Rows of a TMA box of the K pages, or 1: page sizes that go without TMA.
 int paged_prefill_box(int page_size);
-// tk: map of the K pages [n_pages][n_kv][page_size][head_dim] with boxes of
-// paged_prefill_box rows x 64 dims (unused where that is 1).
-cudaError_t launch_paged_prefill(const PagedAttnArgs& a, const CUtensorMap& tk, int head_dim, int dtype, int num_sms,
-                                 cudaStream_t s, bool join);
+// tk, tv: maps of the K and V pages [n_pages][n_kv][page_size][head_dim] with
+// boxes of paged_prefill_box rows x 64 dims (unused where that is 1).
+cudaError_t launch_paged_prefill(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
+                                 int dtype, int num_sms, cudaStream_t s, bool join);
+cudaError_t launch_paged_prefill_pair(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int dtype,
+                                      int64_t n_slots, int n_split, int num_sms, cudaStream_t s);
 
 }  // namespace qsa
