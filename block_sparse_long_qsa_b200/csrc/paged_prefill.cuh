@@ -65,11 +65,16 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
     }
   }
 }
-// One arrival on the same barrier of the pair's first CTA.
+// One arrival on the same barrier of the pair's first CTA.  MEMORY: it also
+// releases this thread's shared-memory writes to the pair (a wait of about 1000
+// cycles for all writes in flight); without, it orders what tcgen05 waits and
+// fences have completed: accesses to TMEM.
+template <bool MEMORY>
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+  if (MEMORY) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+  else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
 }
 // The barrier's phase waits for this thread's copies so far, beside its counted
 // arrivals (this form adds the arrival that it makes to the pending count).
@@ -320,7 +325,7 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
       if (PAIR) {                                 // the next S may overwrite these
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader(bar.s_empty);
+        if (lane == 0) arrive_leader<false>(bar.s_empty);
       }
       if (!whole) {
         const uint32_t bits[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
@@ -409,7 +414,7 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (PAIR) arrive_leader(&bar.p_full[buf]);
+        if (PAIR) arrive_leader<false>(&bar.p_full[buf]);
         else mbar_arrive(&bar.p_full[buf]);
       }
     }
@@ -462,7 +467,7 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
-      if (PAIR) arrive_leader(bar.o_empty);
+      if (PAIR) arrive_leader<false>(bar.o_empty);
       else mbar_arrive(bar.o_empty);
     }
     ++items_done;

@@ -223,7 +223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
       fence_async_proxy();                          // written by cp.async, read by the MMA
       if (rank == 1) {
         __syncwarp();
-        if (lane == 0) arrive_leader(q_peer);
+        if (lane == 0) arrive_leader<true>(q_peer);
       } else if (!wait_pair(q_peer, items_done & 1)) {
         ok = false;
         break;
@@ -232,7 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
         if (!wait(&k_full[ks], kph)) { ok = false; break; }
         if (rank == 1) {
           fence_async_proxy();
-          if (lane == 0) arrive_leader(&k_peer[ks]);
+          if (lane == 0) arrive_leader<true>(&k_peer[ks]);
         } else {
           if (!wait_pair(&k_peer[ks], kph)) { ok = false; break; }
           // once the softmax has the scores before in its registers
@@ -286,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
           }
         }
         if (rank == 1) {
-          if (lane == 0) arrive_leader(&v_peer[vs]);
+          if (lane == 0) arrive_leader<true>(&v_peer[vs]);
         } else {
           if (!wait_pair(&v_peer[vs], vph) || !wait_pair(&p_full[count & 1], (count >> 1) & 1)) { ok = false; break; }
           if (i == 0 && items_done > 0 && !wait_pair(o_empty, (items_done - 1) & 1)) { ok = false; break; }
