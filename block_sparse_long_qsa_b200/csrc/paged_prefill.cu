@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
                              (std::is_same<E, __half>::value ? ~((1u << 7) | (1u << 10)) : ~0u);   // f16: 0
   constexpr uint32_t IDESC_PV = ((IDESC & ~(63u << 17)) | ((uint32_t)(D >> 3) << 17)) | (1u << 16);   // V MN-major
   using X = Elem<E>;
+  using TM = Tmem<D, false>;
   const PagedAttnArgs& a = x.a;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
@@ -75,7 +76,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   uint64_t* q_full = v_empty + NS;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_empty + 1;                   // [2]
-  uint64_t* p_full = s_full + 2;                    // [2]
+  uint64_t* s_empty = s_full + 2;                   // [2] (P apart from S)
+  uint64_t* p_full = s_empty + 2;                   // [2]
   uint64_t* pv_done = p_full + 2;                   // [2]
   uint64_t* o_empty = pv_done + 2;
   uint64_t* hand = o_empty + 1;                     // [2][4]: the maximum after a tile, 32 rows each
@@ -98,7 +100,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     }
     mbar_init(q_full, LWARPS);
     mbar_init(q_empty, 1);
-    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 4); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1); }
     for (int i = 0; i < 8; ++i) mbar_init(&hand[i], 1);
     mbar_init(o_empty, 8);
     for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 2);
@@ -327,10 +329,14 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       if (!wait(q_full, items_done & 1)) { ok = false; break; }
       fence_async_proxy();                          // Q: written by cp.async, read by the MMA
       for (int i = 0; i < n_tiles; ++i, ++count) {
-        // S overwrites the buffer of the P two tiles before: its P V is done.
-        // (That barrier's next phase needs this S, so its parity is exact.)
-        if (count >= 2 && !wait(&pv_done[count & 1], ((count >> 1) - 1) & 1)) { ok = false; break; }
-        const uint32_t d = tm + TM_S + 128 * (count & 1);
+        // S overwrites what the buffer had two tiles before: the scores, which are
+        // in registers by now, or P in their place, whose P V is done.  (Either
+        // barrier's next phase needs this S, so the parity is exact.)
+        if (count >= 2 && !wait(TM::APART ? &s_empty[count & 1] : &pv_done[count & 1], ((count >> 1) - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const uint32_t d = tm + TM::s(count & 1);
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
           if (ch % GR == 0) {
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       if (n_tiles <= 0) continue;
       if (items_done > 0 && !wait(o_empty, (items_done - 1) & 1)) { ok = false; break; }
       for (int i = 0; i < n_tiles; ++i, ++count) {
-        const uint32_t p = tm + TM_S + 128 * (count & 1);
+        const uint32_t p = tm + TM::p(count & 1);
         if (!wait(&p_full[count & 1], (count >> 1) & 1)) { ok = false; break; }
 #pragma unroll
         for (int s = 0; s < NCH; ++s) {
@@ -385,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
           const uint32_t vb = base + OFF_V + vslot * SLOT;
 #pragma unroll
           for (int ks = 0; ks < KV / 16; ++ks)
-            umma_ts(tm + TM_O, p + 8 * (s * (KV / 16) + ks), desc_at(desc_mn(KV * 128), vb + 2048 * ks), IDESC_PV,
+            umma_ts(tm + TM::O, p + 8 * (s * (KV / 16) + ks), desc_at(desc_mn(KV * 128), vb + 2048 * ks), IDESC_PV,
                     i > 0 || s > 0 || ks > 0 ? 1u : 0u);
           umma_commit(&v_empty[vslot]);
           if (++vslot == NS) vslot = 0;
@@ -400,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   } else if (warp < W_LOAD) {
     // ---------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
-    softmax_role<E, D, M, false>(x, smem, OFF_OK, OFF_XCH, {s_full, nullptr, p_full, pv_done, hand, xbar, o_empty}, tmem, warp,
+    softmax_role<E, D, M, false>(x, smem, OFF_OK, OFF_XCH, {s_full, s_empty, p_full, pv_done, hand, xbar, o_empty}, tmem, warp,
                                  lane, 0, blockIdx.x, gridDim.x, n_items, abort_flag);
   }
   tc_fence_before();

@@ -20,8 +20,17 @@ constexpr int RT = LOADERS / 8, RJ = KT / RT;       // cp.async: rows of a pass,
 // ring holds 5), S 2 ahead of the softmax
 constexpr int NOK = 16;
 constexpr uint32_t TMEM_COLS = 512;
-// One CTA: S / P buffers at columns 0 and 128.  Pair: S at 0, P at 128 and 192.
-constexpr uint32_t TM_S = 0, TM_P = 128, TM_O = 256;
+// TMEM columns.  Where they suffice, P has two buffers (64 columns) apart from S
+// (128), so that S is free as soon as its scores are in registers: with O of up to
+// 128 columns S has two buffers, in a pair (256) one.  One CTA with 256 columns of
+// O has two buffers in which P replaces the scores.
+template <int D, bool PAIR>
+struct Tmem {
+  static constexpr bool APART = PAIR || D <= 128;
+  static constexpr uint32_t O = D <= 128 ? 384 : 256;
+  static __device__ __forceinline__ uint32_t s(uint32_t buf) { return PAIR ? 0 : 128 * buf; }
+  static __device__ __forceinline__ uint32_t p(uint32_t buf) { return PAIR ? 128 + 64 * buf : APART ? 256 + 64 * buf : 128 * buf; }
+};
 constexpr int MAX_PIECES = 160;                     // bound of the scratch, pieces of 128 rows
 constexpr int MAX_SPLIT = 32;
 constexpr float RAISE = 8.f;                        // lazy maximum: P stays below 2^8
@@ -30,10 +39,8 @@ __device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t c16) {
   return row * 128u + ((c16 ^ (row & 7u)) << 4);
 }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// mbar_wait with the thread suspended for up to 10 us at a time instead of
-// polling: sixteen warps that poll slow the others' shared-memory and
-// special-function instructions.
-// CLUSTER: the arrivals may come from the other CTA of a pair.
+// mbar_wait that sees an abort at once.  CLUSTER: the arrivals may come from the
+// other CTA of a pair.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
   uint64_t t0 = 0;
@@ -42,19 +49,13 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
     if (CLUSTER)
       asm volatile(
           "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
           "selp.u32 %0, 1, 0, p;\n\t}"
           : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+          : "r"(smem_u32(bar)), "r"(parity)
           : "memory");
     else
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
-          : "memory");
+      ok = mbar_try_wait(bar, parity);
     if (ok) return true;
     if (it == 0) t0 = globaltimer();
     if (*abort_flag) return false;
@@ -257,9 +258,8 @@ struct Item {
 };
 
 // The softmax warps (0-7): row r0 + r of an item of ROWS rows in TMEM lane r, items
-// w0, w0 + w_step, ..  In a pair of CTAs (PAIR) S has one buffer, which is free as
-// soon as the scores are in registers, P has two of its own, and the MMA's
-// barriers are the first CTA's.
+// w0, w0 + w_step, ..  In a pair of CTAs (PAIR) the MMA's barriers are the first
+// CTA's.
 struct SoftBars {
   uint64_t *s_full, *s_empty, *p_full, *pv_done, *hand, *xbar, *o_empty;
 };
@@ -268,6 +268,7 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
                                              uint32_t tmem, int warp, int lane, int r0, int64_t w0, int64_t w_step,
                                              int64_t n_items, volatile int* abort_flag) {
   using X = Elem<E>;
+  using TM = Tmem<D, PAIR>;
   const PagedAttnArgs& a = x.a;
   const int per = a.hq / a.hk;
   const int quad = warp & 3, wg = warp >> 2;      // rows 32 quad .., tiles with count % 2 == wg
@@ -309,8 +310,7 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
       const uint32_t n = count + i, buf = wg;     // n % 2 == wg
       if (!wait(&bar.s_full[buf], (n >> 1) & 1)) { ok = false; break; }
       tc_fence_after();
-      const uint32_t s_addr = tmem + lanes + TM_S + (PAIR ? 0 : 128 * buf);
-      const uint32_t p_addr = tmem + lanes + (PAIR ? TM_P + 64 * buf : TM_S + 128 * buf);
+      const uint32_t s_addr = tmem + lanes + TM::s(buf), p_addr = tmem + lanes + TM::p(buf);
       float s[4][32];
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, s[q]);
@@ -322,10 +322,13 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
                          (t0.x & t0.y & t0.z & t0.w & t1.x & t1.y & t1.z & t1.w) == 0x0f0f0f0fu;
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_ld_wait(s[q]);
-      if (PAIR) {                                 // the next S may overwrite these
+      if (TM::APART) {                            // a later S may overwrite these
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader<false>(bar.s_empty);
+        if (lane == 0) {
+          if (PAIR) arrive_leader<false>(bar.s_empty);
+          else mbar_arrive(&bar.s_empty[buf]);
+        }
       }
       if (!whole) {
         const uint32_t bits[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
@@ -378,7 +381,7 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
 #pragma unroll 1
           for (int cc = 0; cc < D / 16; ++cc) {
             uint32_t o[16];
-            const uint32_t ad = tmem + lanes + TM_O + 16 * cc;
+            const uint32_t ad = tmem + lanes + TM::O + 16 * cc;
             tmem_ld16(ad, o);                     // waits for the load
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
@@ -388,7 +391,7 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
       }
       // the P of two tiles before has been used (where P shares the scores'
       // columns, this tile's S came after that)
-      if (PAIR && n >= 2 && !wait(&bar.pv_done[buf], ((n >> 1) - 1) & 1)) { ok = false; break; }
+      if (TM::APART && n >= 2 && !wait(&bar.pv_done[buf], ((n >> 1) - 1) & 1)) { ok = false; break; }
       // p = 2^(s scale - m); the sum takes the fp32 values, the products p
       // rounded to 16 bits
       const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-m, -m);
@@ -444,7 +447,7 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
     for (int cc = 0; cc < D / 64; ++cc) {
       float o[32];
       const int d0 = (D / 2) * wg + 32 * cc;
-      tmem_ld32(tmem + lanes + TM_O + d0, o);
+      tmem_ld32(tmem + lanes + TM::O + d0, o);
       tmem_ld_wait(o);
       if (orow >= 0 && part) {
         float4* dst = reinterpret_cast<float4*>(sc.o + orow * D + d0);

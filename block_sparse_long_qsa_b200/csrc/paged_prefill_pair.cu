@@ -42,6 +42,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
   constexpr uint32_t IDESC = umma_idesc_bf16_f32(M, KT) &
                              (std::is_same<E, __half>::value ? ~((1u << 7) | (1u << 10)) : ~0u);   // f16: 0
   constexpr uint32_t IDESC_PV = ((IDESC & ~(63u << 17)) | ((uint32_t)(D >> 3) << 17)) | (1u << 16);   // V MN-major
+  using TM = Tmem<D, true>;
   const PagedAttnArgs& a = x.a;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);   // [NK] this CTA's half
@@ -241,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
           const uint32_t kb = base + OFF_K + ks * STAGE;
 #pragma unroll
           for (int e = 0; e < D / 16; ++e)
-            umma_ss<2>(tm + TM_S, desc_at(DESC_K, base + (e >> 2) * 16384 + 32 * (e & 3)),
+            umma_ss<2>(tm + TM::s(0), desc_at(DESC_K, base + (e >> 2) * 16384 + 32 * (e & 3)),
                        desc_at(DESC_K, kb + (e >> 2) * 8192 + 32 * (e & 3)), IDESC, e > 0 ? 1u : 0u);
           umma_commit<2>(&k_empty[ks]);
           umma_commit<2>(&s_full[count & 1]);
@@ -291,10 +292,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
           if (!wait_pair(&v_peer[vs], vph) || !wait_pair(&p_full[count & 1], (count >> 1) & 1)) { ok = false; break; }
           if (i == 0 && items_done > 0 && !wait_pair(o_empty, (items_done - 1) & 1)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t vb = base + OFF_V + vs * STAGE, p = tm + TM_P + 64 * (count & 1);
+          const uint32_t vb = base + OFF_V + vs * STAGE, p = tm + TM::p(count & 1);
 #pragma unroll
           for (int e = 0; e < KT / 16; ++e)
-            umma_ts<2>(tm + TM_O, p + 8 * e, desc_at(desc_mn(16384), vb + 2048 * e), IDESC_PV, i > 0 || e > 0 ? 1u : 0u);
+            umma_ts<2>(tm + TM::O, p + 8 * e, desc_at(desc_mn(16384), vb + 2048 * e), IDESC_PV, i > 0 || e > 0 ? 1u : 0u);
           umma_commit<2>(&v_empty[vs]);
           umma_commit<2>(&pv_done[count & 1]);
         }
