@@ -53,7 +53,7 @@ constexpr uint32_t OFF_V = OFF_K + NS * SLOT;
 constexpr uint32_t OFF_XCH = OFF_V + NS * SLOT;     // running maxima [2][128], row sums [2][128]
 constexpr uint32_t OFF_OK = OFF_XCH + 2048;         // rows that are there, of NOK tiles, 32 bytes each
 constexpr uint32_t OFF_BAR = OFF_OK + 32 * NOK;
-constexpr uint32_t SMEM = OFF_BAR + 384;
+constexpr uint32_t SMEM = OFF_BAR + 448;
 static_assert(SMEM <= 232448, "prefill smem");
 
 template <class E, int D, bool TMA>
@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   uint64_t* pv_done = p_full + 2;                   // [2]
   uint64_t* o_empty = pv_done + 2;
   uint64_t* hand = o_empty + 1;                     // [2][4]: the maximum after a tile, 32 rows each
-  uint64_t* xbar = hand + 8;                        // [4]: row sums, 32 rows each
+  uint64_t* turn = hand + 8;                        // [2][4]: the exponentials of a tile
+  uint64_t* xbar = turn + 8;                        // [4]: row sums, 32 rows each
   uint64_t* mma_done = xbar + 4;                    // [2]: the S and the P V issuer
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     mbar_init(q_full, LWARPS);
     mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 4); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1); }
-    for (int i = 0; i < 8; ++i) mbar_init(&hand[i], 1);
+    for (int i = 0; i < 8; ++i) { mbar_init(&hand[i], 1); mbar_init(&turn[i], 1); }
     mbar_init(o_empty, 8);
     for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 2);
     mbar_init(&mma_done[0], 1);
@@ -138,33 +139,63 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
       const int64_t head = (int64_t)it.g * a.kv.head_stride + 8 * c;
       auto key_of = [&](int v) { return v < it.ns ? v : it.lo + (v - it.ns); };
-      // Page ids of this thread's rows rt + RT j of a tile: loaded a tile ahead,
-      // all at once.
-      int ids[RJ];
-      auto load_ids = [&](int tile) {
-#pragma unroll
-        for (int j = 0; j < RJ; ++j) {
-          const int key = key_of(max(min(tile * KT + RT * j + rt, it.n_vis - 1), 0));
-          ids[j] = __ldg(table + page_of(a.kv, (uint32_t)min(key, a.kv.capacity - 1)));
-        }
-      };
       // A tile's rows: offset of this thread's chunk, and whether the row is there
       // (some query sees it and its page is one).
       struct Rows { int64_t off[RJ]; uint32_t ok; };
+      // Page ids are loaded a tile ahead, all at once.  With TMA the 16 rows of a
+      // pass lie in one page (page size and numbering are multiples of 16): lane j
+      // finds pass j, the others take its place by a shuffle.  Else each thread
+      // finds its rows rt + RT j.
+      constexpr int NI = TMA ? 1 : RJ;
+      int ids[NI];
+      const int pass = lane % RJ;
+      auto load_ids = [&](int tile) {
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          const int v = tile * KT + (TMA ? RT * pass : RT * j + rt);
+          const int key = key_of(max(min(v, it.n_vis - 1), 0));
+          ids[j] = __ldg(table + page_of(a.kv, (uint32_t)min(key, a.kv.capacity - 1)));
+        }
+      };
+      auto in_page = [&](int key) -> int64_t {
+        return (int64_t)(key - (int)(page_of(a.kv, (uint32_t)key) * (uint32_t)a.kv.page_size)) * a.kv.token_stride;
+      };
+      auto needed = [&](int v, int key) { return v < it.n_vis && (key >= it.first || key < a.sinks); };
+      const int64_t mine = head + (int64_t)rt * a.kv.token_stride;
       auto find_rows = [&](int tile, Rows& d) {
         d.ok = 0;
-        uint32_t bad = 0;
+        if constexpr (TMA) {
+          const int v = tile * KT + RT * pass, key = key_of(v);
+          const bool any = v < it.n_vis && (key + RT > it.first || key < a.sinks);
+          const bool good = any && (uint32_t)ids[0] < (uint32_t)a.kv.n_pages;
+          if (any && !good) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
+          const bool clean = good && v + RT <= it.n_vis && (key >= it.first || key + RT <= a.sinks);
+          const int64_t off = good ? (int64_t)ids[0] * a.kv.page_stride + in_page(key) : 0;
 #pragma unroll
-        for (int j = 0; j < RJ; ++j) {
-          const int v = tile * KT + RT * j + rt, key = key_of(v);
-          const bool needed = v < it.n_vis && (key >= it.first || key < a.sinks);
-          const bool good = needed && (uint32_t)ids[j] < (uint32_t)a.kv.n_pages;
-          const int in_page = key - (int)(page_of(a.kv, (uint32_t)key) * (uint32_t)a.kv.page_size);
-          d.off[j] = good ? (int64_t)ids[j] * a.kv.page_stride + (int64_t)in_page * a.kv.token_stride + head : 0;
-          d.ok |= (uint32_t)good << j;
-          bad |= (uint32_t)(needed && !good);
+          for (int j = 0; j < RJ; ++j) d.off[j] = __shfl_sync(0xffffffffu, off, j) + mine;
+          if (__all_sync(0xffffffffu, clean)) {
+            d.ok = (1u << RJ) - 1;
+          } else {
+            const uint32_t there = __ballot_sync(0xffffffffu, good);
+#pragma unroll
+            for (int j = 0; j < RJ; ++j) {
+              const int r = tile * KT + RT * j + rt;
+              const bool ok = (there >> j & 1) && needed(r, key_of(r));
+              d.ok |= (uint32_t)ok << j;
+            }
+          }
+        } else {
+          bool bad = false;
+#pragma unroll
+          for (int j = 0; j < RJ; ++j) {
+            const int v = tile * KT + RT * j + rt, key = key_of(v);
+            const bool want = needed(v, key), good = want && (uint32_t)ids[j] < (uint32_t)a.kv.n_pages;
+            d.off[j] = good ? (int64_t)ids[j] * a.kv.page_stride + in_page(key) + head : 0;
+            d.ok |= (uint32_t)good << j;
+            bad |= want && !good;
+          }
+          if (bad) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
         }
-        if (bad) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
       };
       const uint32_t lane_dst = swz128(rt, c);         // rows of a pass are 16 apart: the same swizzle in each
       auto load_k = [&](const Rows& d) -> bool {
@@ -406,7 +437,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   } else if (warp < W_LOAD) {
     // ---------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
-    softmax_role<E, D, M, false>(x, smem, OFF_OK, OFF_XCH, {s_full, s_empty, p_full, pv_done, hand, xbar, o_empty}, tmem, warp,
+    softmax_role<E, D, M, false>(x, smem, OFF_OK, OFF_XCH, {s_full, s_empty, p_full, pv_done, hand, turn, xbar, o_empty}, tmem, warp,
                                  lane, 0, blockIdx.x, gridDim.x, n_items, abort_flag);
   }
   tc_fence_before();

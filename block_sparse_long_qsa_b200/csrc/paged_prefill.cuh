@@ -33,6 +33,11 @@ struct Tmem {
 };
 constexpr int MAX_PIECES = 160;                     // bound of the scratch, pieces of 128 rows
 constexpr int MAX_SPLIT = 32;
+// Quarter of a tile's exponentials after which the next tile's begin (32K tokens
+// of 24 + 2 heads of 256: 9.65 ms with 1, 9.85 with 2, 9.87 without turns; 16K of
+// 16 heads of 64: 1.20 ms with 1, 1.19 with 2, 1.27 without; 128: 3.0 ms with 1,
+// 2.6 with 2 and without).
+__host__ __device__ constexpr int turn_after(int D) { return D == 256 ? 1 : 2; }
 constexpr float RAISE = 8.f;                        // lazy maximum: P stays below 2^8
 
 __device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t c16) {
@@ -261,7 +266,7 @@ struct Item {
 // w0, w0 + w_step, ..  In a pair of CTAs (PAIR) the MMA's barriers are the first
 // CTA's.
 struct SoftBars {
-  uint64_t *s_full, *s_empty, *p_full, *pv_done, *hand, *xbar, *o_empty;
+  uint64_t *s_full, *s_empty, *p_full, *pv_done, *hand, *turn, *xbar, *o_empty;
 };
 template <class E, int D, int ROWS, bool PAIR>
 __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint32_t off_ok, uint32_t off_xch, const SoftBars& bar,
@@ -392,6 +397,10 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
       // the P of two tiles before has been used (where P shares the scores'
       // columns, this tile's S came after that)
       if (TM::APART && n >= 2 && !wait(&bar.pv_done[buf], ((n >> 1) - 1) & 1)) { ok = false; break; }
+      // The exponentials of a tile begin when those of the tile before are nearly
+      // done.  The two warps of a scheduler share its special-function unit: side
+      // by side they would take twice as long and leave it idle afterwards.
+      if (n > 0 && !wait(&bar.turn[(wg ^ 1) * 4 + quad], ((n - 1) >> 1) & 1)) { ok = false; break; }
       // p = 2^(s scale - m); the sum takes the fp32 values, the products p
       // rounded to 16 bits
       const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-m, -m);
@@ -409,6 +418,10 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
           pk[e] = X::pack(x0, x1);
         }
         tmem_st16(p_addr + 16 * q, pk);
+        if (q == turn_after(D)) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.turn[wg * 4 + quad]);
+        }
       }
       float l0, l1;
       upk2(sum, l0, l1);

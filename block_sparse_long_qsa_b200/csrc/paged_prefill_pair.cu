@@ -30,7 +30,7 @@ constexpr uint32_t OFF_V = OFF_K + NK * STAGE;
 constexpr uint32_t OFF_XCH = OFF_V + NV * STAGE;
 constexpr uint32_t OFF_OK = OFF_XCH + 2048;
 constexpr uint32_t OFF_BAR = OFF_OK + 32 * NOK;
-constexpr uint32_t SMEM = OFF_BAR + 384;
+constexpr uint32_t SMEM = OFF_BAR + 448;
 static_assert(SMEM <= 232448, "prefill smem");
 
 __device__ __forceinline__ void cluster_sync() {
@@ -60,7 +60,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
   uint64_t* pv_done = p_full + 2;                   // [2]
   uint64_t* o_empty = pv_done + 2;
   uint64_t* hand = o_empty + 1;                     // [2][4]
-  uint64_t* xbar = hand + 8;                        // [4]
+  uint64_t* turn = hand + 8;                        // [2][4]: the exponentials of a tile
+  uint64_t* xbar = turn + 8;                        // [4]
   uint64_t* mma_done = xbar + 4;                    // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -76,7 +77,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
     for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8); mbar_init(&pv_done[i], 1); }
     mbar_init(s_empty, 8);
     mbar_init(o_empty, 16);
-    for (int i = 0; i < 8; ++i) mbar_init(&hand[i], 1);
+    for (int i = 0; i < 8; ++i) { mbar_init(&hand[i], 1); mbar_init(&turn[i], 1); }
     for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 2);
     mbar_init(&mma_done[0], 1);
     mbar_init(&mma_done[1], 1);
@@ -308,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
   } else if (warp < W_LOAD) {
     // ---------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
-    softmax_role<E, D, M, true>(x, smem, OFF_OK, OFF_XCH, {s_full, s_empty, p_full, pv_done, hand, xbar, o_empty}, tmem, warp,
+    softmax_role<E, D, M, true>(x, smem, OFF_OK, OFF_XCH, {s_full, s_empty, p_full, pv_done, hand, turn, xbar, o_empty}, tmem, warp,
                                 lane, 128 * rank, w0, w_step, n_items, abort_flag);
   }
   tc_fence_before();
