@@ -6,7 +6,7 @@
 // over the keys j up to the token's own that window and sinks leave; one pass
 // with a running maximum and sum.
 //
-// Item = (128 query rows of one sequence, KV head, range of keys); the rows are
+// Item = (128 query rows of one sequence, KV head); the rows are
 // the sequence's (token, query head of the KV head) pairs laid out flat, so any
 // head count fills the tiles and the heads of a KV head share its loads.  The
 // keys that any row sees are numbered without the gap between sinks and window
@@ -30,15 +30,16 @@
 //     bytes a cycle), four warps of cp.async bring 32.
 //   * warp 12: S(i) = Q K^T (M = 128, N = 128); warp 14: O += P V (N = D).  Two
 //     issuers, so a ready P V never waits behind the next S.
-// Registers: 168 a softmax thread, 88 the others (setmaxnreg).
+// Registers: 184 a softmax thread, 72 the others (setmaxnreg; 168 and 88: 4 % slower).
 // Every mbarrier wait is bounded (timeout -> error word, clean exit): on an abort
 // every role leaves its loop, the loaders wait for their own copies and the MMA
 // thread for its last commit before TMEM is released.
 //
-// With few rows (a short chunk over a long prefix) an item's keys are cut into
-// n_split ranges so that the SMs fill up; the ranges' results go to the scratch
-// as normalised fp32 rows with their log-sum-exp, and the join kernel adds them
-// in the order of the keys.
+// Balance: with few items their tiles, laid end to end, are cut evenly over the
+// CTAs, so a short chunk over a long prefix and batches of any mix of lengths keep
+// every SM busy.  A CTA's piece of an item that it shares goes to the scratch as
+// normalised fp32 rows with their log-sum-exp; the join kernel adds the pieces in
+// the order of the keys.  Many items are dealt out whole.
 #include "paged_prefill.cuh"
 
 namespace qsa {
@@ -56,7 +57,7 @@ constexpr uint32_t OFF_BAR = OFF_OK + 32 * NOK;
 constexpr uint32_t SMEM = OFF_BAR + 448;
 static_assert(SMEM <= 232448, "prefill smem");
 
-template <class E, int D, bool TMA>
+template <class E, int D, bool TMA, bool EVEN>
 __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_constant__ Args x) {
   constexpr int NCH = D / 64;                       // 64-dim chunks: K (and V) slots of a tile
   constexpr int KV = KT / NCH;                      // keys of a V slot
@@ -113,10 +114,15 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   if (warp == W_MMA) { tmem_alloc(tmem_slot, TMEM_COLS); tmem_relinquish(); }
   pdl_launch();
   tc_fence_before();
+  // (without EVEN the walk is of launch constants, not through a structure that
+  // the roles' loops would have to read)
+  Walk walk{};
+  if constexpr (EVEN) walk = uniform(make_walk<M>(x, blockIdx.x, gridDim.x, smem));   // in Q's place
+  const int64_t w_first = EVEN ? walk.w : (int64_t)blockIdx.x, w_step = EVEN ? walk.step : (int64_t)gridDim.x;
+  const int64_t w_last = EVEN ? walk.last : x.n_slots * x.a.hk - 1;
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int64_t n_items = x.grid.n_slots * a.hk * x.grid.n_split;
   const int per = a.hq / a.hk;
 
   if (warp >= W_LOAD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
@@ -133,8 +139,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
-      const Item<M> it(x, w);
+    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+      const Item<M> it = item_of<M, EVEN>(x, walk, w);
       if (it.n_tiles <= 0) continue;
       const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
       const int64_t head = (int64_t)it.g * a.kv.head_stride + 8 * c;
@@ -290,8 +296,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     uint32_t landing = 0, open = 0;                // groups that copies went to; arrivals of an unfinished one
     bool ok = true;
     const int box = x.box, nb = KT / box;
-    for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
-      const Item<M> it(x, w);
+    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+      const Item<M> it = item_of<M, EVEN>(x, walk, w);
       if (it.n_tiles <= 0) continue;
       const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
       // lane i has box i of a tile (lanes past the last repeat): its page, or -1
@@ -353,8 +359,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
     };
-    for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
-      const Item<M> it(x, w);
+    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+      const Item<M> it = item_of<M, EVEN>(x, walk, w);
       const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
       if (n_tiles <= 0) continue;
       if (!wait(q_full, items_done & 1)) { ok = false; break; }
@@ -403,8 +409,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
     };
-    for (int64_t w = blockIdx.x; ok && w < n_items; w += gridDim.x) {
-      const Item<M> it(x, w);
+    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+      const Item<M> it = item_of<M, EVEN>(x, walk, w);
       const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
       if (n_tiles <= 0) continue;
       if (items_done > 0 && !wait(o_empty, (items_done - 1) & 1)) { ok = false; break; }
@@ -437,8 +443,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   } else if (warp < W_LOAD) {
     // ---------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
-    softmax_role<E, D, M, false>(x, smem, OFF_OK, OFF_XCH, {s_full, s_empty, p_full, pv_done, hand, turn, xbar, o_empty}, tmem, warp,
-                                 lane, 0, blockIdx.x, gridDim.x, n_items, abort_flag);
+    softmax_role<E, D, M, false, EVEN>(x, smem, OFF_OK, OFF_XCH, {s_full, s_empty, p_full, pv_done, hand, turn, xbar, o_empty}, tmem, warp,
+                                 lane, 0, walk, w_first, w_last, w_step, blockIdx.x, abort_flag);
   }
   tc_fence_before();
   __syncthreads();
@@ -448,42 +454,56 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   }
 }
 
-// Joins the ranges of items whose keys were cut: one warp a query row.
+// Joins the pieces of the item that starts in CTA (or pair) blockIdx.x and goes on
+// after it, in order; one warp a query row.
 template <class E, int D, int M>
 __global__ void __launch_bounds__(256) paged_prefill_join_kernel(const __grid_constant__ Args x) {
   constexpr int W = D / 32;                         // dims of a lane: 2, 4 or 8
   using X = Elem<E>;
   const PagedAttnArgs& a = x.a;
   pdl_wait();
-  const int64_t id = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5));
-  const int64_t w0 = id / M * x.grid.n_split;       // the item's first range
-  const int r = (int)(id % M), lane = threadIdx.x & 31;
-  if (w0 >= x.grid.n_slots * a.hk * x.grid.n_split) return;
-  const Item<M> it(x, w0);
-  if (it.n_tiles <= 0 || it.pieces <= 1 || r >= it.rows) return;
   const Scratch sc = scratch_of(a.scratch);
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const JoinRec rec = sc.rec[c];
+  if (rec.last < 0) return;
+  const Item<M> it(x, rec.w);
+  const int n = rec.last - c + 1;
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (r >= it.rows) return;
+  auto row_of = [&](int i) { return (int64_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * M + r; };
   float m = -FLT_MAX, l = 0.f, acc[W];
 #pragma unroll
   for (int e = 0; e < W; ++e) acc[e] = 0.f;
-  for (int i = 0; i < it.pieces; ++i) {
-    const int64_t row = (w0 + i) * M + r;
-    const float z = sc.lse2[row];
-    float v[W];
+  for (int i0 = 0; i0 < n; i0 += 32) {              // lane i: the weight of piece i0 + i
+    const float z = i0 + lane < n ? sc.lse2[row_of(i0 + lane)] : -INFINITY;
+    float nm = fmaxf(m, z);
 #pragma unroll
-    for (int e = 0; e < W; ++e) v[e] = sc.o[row * D + W * lane + e];
-    if (z == -INFINITY) continue;                   // a range without a key
-    const float nm = fmaxf(m, z), f0 = exp2_approx(m - nm), f1 = exp2_approx(z - nm);
-    l = fmaf(l, f0, f1);
-#pragma unroll
-    for (int e = 0; e < W; ++e) acc[e] = fmaf(acc[e], f0, v[e] * f1);
+    for (int o = 16; o > 0; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
+    const float f = exp2_approx(m - nm), wz = z == -INFINITY ? 0.f : exp2_approx(z - nm);
     m = nm;
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < W; ++e) acc[e] *= f;
+    const int k = min(32, n - i0);
+#pragma unroll 8
+    for (int i = 0; i < k; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, wz, i);
+      const float2* src = reinterpret_cast<const float2*>(sc.o + row_of(i0 + i) * D) + lane;
+      l += wi;
+#pragma unroll
+      for (int e = 0; e < W / 2; ++e) {               // dims 64 e + 2 lane, + 1
+        const float2 v = src[32 * e];
+        acc[2 * e] = fmaf(wi, v.x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(wi, v.y, acc[2 * e + 1]);
+      }
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int per = a.hq / a.hk;
   const int64_t flat = it.row0 + r, orow = (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + W * lane);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D) + lane;
 #pragma unroll
-  for (int e = 0; e < W / 2; ++e) dst[e] = X::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  for (int e = 0; e < W / 2; ++e) dst[32 * e] = X::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
   if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
@@ -493,38 +513,43 @@ bool use_pair(const PagedAttnArgs& a, int head_dim) {
   return head_dim == 256 && paged_prefill_box(a.kv.page_size) > 1 && a.T * (a.hq / a.hk) >= PAIR_ROWS * a.B;
 }
 
-Grid grid_of(const PagedAttnArgs& a, int head_dim, int num_sms) {
-  const bool pair = use_pair(a, head_dim);
-  const int m = pair ? 256 : 128;
-  Grid g;
-  g.n_slots = (a.T * (a.hq / a.hk) + m - 1) / m + a.B;
-  // ranges: as many as fill the SMs, from the slots (a sequence's last slot is
-  // often empty, so the SMs are filled to about a half at the least)
-  const int sms = num_sms < MAX_PIECES ? num_sms : MAX_PIECES;
-  const int64_t n = (pair ? sms / 2 : sms) / (g.n_slots * a.hk);
-  g.n_split = (int)(n < 1 ? 1 : (n > MAX_SPLIT ? MAX_SPLIT : n));
-  return g;
+// Tile slots of the batch, and the CTAs (or pairs) that walk them.
+int64_t slots_of(const PagedAttnArgs& a, int head_dim) {
+  const int m = use_pair(a, head_dim) ? 256 : 128;
+  return (a.T * (a.hq / a.hk) + m - 1) / m + a.B;
+}
+int walkers_of(const PagedAttnArgs& a, int head_dim, int num_sms) {
+  const int most = num_sms < MAX_CTAS ? num_sms : MAX_CTAS;
+  return use_pair(a, head_dim) ? most / 2 : most;
+}
+// Whether items may be cut over the CTAs: with no more than two to a CTA one long
+// sequence among them would keep a CTA busy long after the others (64 x 5 tokens
+// over 2000 to 30000 keys: 631 us whole, 250 cut).  With more, or where whole items
+// are quicker after all, it costs 4 to 7 us to find out.
+bool may_cut(const PagedAttnArgs& a, int head_dim, int num_sms) {
+  const int64_t items = slots_of(a, head_dim) * a.hk;
+  return paged_prefill_box(a.kv.page_size) > 1 && items <= MAX_EVEN && items <= 2 * walkers_of(a, head_dim, num_sms);
 }
 
-template <class E, int D, bool TMA>
+template <class E, int D, bool TMA, bool EVEN>
 cudaError_t launch_attn(const Args& x, int grid, cudaStream_t s) {
   static bool attr_done[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr_done[dev]) {
-    e = cudaFuncSetAttribute(paged_prefill_kernel<E, D, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+    e = cudaFuncSetAttribute(paged_prefill_kernel<E, D, TMA, EVEN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev] = true;
   }
-  paged_prefill_kernel<E, D, TMA><<<grid, THREADS, SMEM, s>>>(x);
+  paged_prefill_kernel<E, D, TMA, EVEN><<<grid, THREADS, SMEM, s>>>(x);
   return cudaGetLastError();
 }
 
 template <class E, int D, int M>
-cudaError_t launch_join(const Args& x, cudaStream_t s) {
+cudaError_t launch_join(const Args& x, int walkers, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(x.grid.n_slots * x.a.hk * (M / 8)));
+  cfg.gridDim = dim3((unsigned)walkers, M / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -541,25 +566,23 @@ cudaError_t launch_d(const PagedAttnArgs& a, const CUtensorMap& tk, int num_sms,
   x.tk = tk;
   x.tv = tk;
   x.a = a;
-  x.grid = grid_of(a, D, num_sms);
+  x.n_slots = slots_of(a, D);
+  const int walkers = walkers_of(a, D, num_sms);
   x.box = paged_prefill_box(a.kv.page_size);
   if (join) {
     if constexpr (D == 256)
-      if (use_pair(a, D)) return launch_join<E, D, 256>(x, s);
-    return launch_join<E, D, 128>(x, s);
+      if (use_pair(a, D)) return launch_join<E, D, 256>(x, walkers, s);
+    return launch_join<E, D, 128>(x, walkers, s);
   }
-  const int64_t items = x.grid.n_slots * a.hk * x.grid.n_split;
-  const int grid = (int)(items < num_sms ? items : num_sms);
-  return x.box > 1 ? launch_attn<E, D, true>(x, grid, s) : launch_attn<E, D, false>(x, grid, s);
+  if (may_cut(a, D, num_sms)) return launch_attn<E, D, true, true>(x, walkers, s);
+  return x.box > 1 ? launch_attn<E, D, true, false>(x, walkers, s) : launch_attn<E, D, false, false>(x, walkers, s);
 }
 
 }  // namespace
 
-size_t paged_prefill_scratch(int head_dim) { return (size_t)MAX_PIECES * M * (head_dim + 1) * 4; }
+size_t paged_prefill_scratch(int head_dim) { return REC_BYTES + (size_t)2 * MAX_CTAS * 128 * (head_dim + 1) * 4; }
 
-bool paged_prefill_splits(const PagedAttnArgs& a, int head_dim, int num_sms) {
-  return grid_of(a, head_dim, num_sms).n_split > 1;
-}
+bool paged_prefill_splits(const PagedAttnArgs& a, int head_dim, int num_sms) { return may_cut(a, head_dim, num_sms); }
 
 int paged_prefill_box(int page_size) {
   return page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : page_size % 16 == 0 ? 16 : 1;
@@ -569,8 +592,8 @@ cudaError_t launch_paged_prefill(const PagedAttnArgs& a, const CUtensorMap& tk, 
                                  int dtype, int num_sms, cudaStream_t s, bool join) {
   if (a.B <= 0 || a.T <= 0) return cudaSuccess;
   if (!join && use_pair(a, head_dim)) {
-    const Grid g = grid_of(a, head_dim, num_sms);
-    return launch_paged_prefill_pair(a, tk, tv, dtype, g.n_slots, g.n_split, num_sms, s);
+    return launch_paged_prefill_pair(a, tk, tv, dtype, slots_of(a, head_dim), walkers_of(a, head_dim, num_sms),
+                                     may_cut(a, head_dim, num_sms), s);
   }
   const bool bf = dtype == QSA_DTYPE_BF16;
   switch (head_dim) {

@@ -11,7 +11,7 @@ namespace {
 
 constexpr int KT = 128;                             // keys of a tile
 constexpr int THREADS = 512;
-constexpr int REGS_SOFT = 168, REGS_REST = 88;
+constexpr int REGS_SOFT = 184, REGS_REST = 72;
 static_assert(256 * (REGS_SOFT + REGS_REST) <= 65536, "register split");
 constexpr int W_LOAD = 8, LWARPS = 4, W_MMA = 12, W_TMA = 13, W_PV = 14;   // warp 15 only makes up the warpgroup
 constexpr int LOADERS = 32 * LWARPS;
@@ -31,8 +31,14 @@ struct Tmem {
   static __device__ __forceinline__ uint32_t s(uint32_t buf) { return PAIR ? 0 : 128 * buf; }
   static __device__ __forceinline__ uint32_t p(uint32_t buf) { return PAIR ? 128 + 64 * buf : APART ? 256 + 64 * buf : 128 * buf; }
 };
-constexpr int MAX_PIECES = 160;                     // bound of the scratch, pieces of 128 rows
-constexpr int MAX_SPLIT = 32;
+constexpr int MAX_CTAS = 160;                       // bound of the scratch (148 SMs on B200)
+constexpr int MAX_EVEN = THREADS;                   // most items that may be cut over the CTAs
+// In tiles (of about 1.8 us): what an item costs beside its own (its queries, the
+// first scores, the last products and the results); the least that is worth a CTA;
+// what the pieces and their join cost.  (37 tokens over 20K keys: whole items 163
+// tiles in a row, cut 15 and 50 us; 16 x 30 tokens over 1000 keys: whole 14 and 29
+// us, cut 10 and 50 us.)
+constexpr int ITEM_COST = 6, LEAST = 4, JOIN_COST = 15;
 // Quarter of a tile's exponentials after which the next tile's begin (32K tokens
 // of 24 + 2 heads of 256: 9.65 ms with 1, 9.85 with 2, 9.87 without turns; 16K of
 // 16 heads of 64: 1.20 ms with 1, 1.19 with 2, 1.27 without; 128: 3.0 ms with 1,
@@ -192,22 +198,29 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-struct Grid {
-  int64_t n_slots;          // tile slots of the batch
-  int n_split;
-};
+// What CTA (or pair) c leaves for the join: the item that starts in its range and
+// goes on in the next ones'.
+struct JoinRec { int64_t w; int32_t last; };
+// A CTA has up to two pieces of shared items: 2c + 1 of one that starts with it, 2c
+// of one that came in from before; 128 rows of D (a pair's 256) and their base-2
+// log-sum-exp.
 struct Scratch {
-  float* lse2;              // [MAX_PIECES][128]
-  float* o;                 // [MAX_PIECES][128][D]
+  JoinRec* rec;             // [MAX_CTAS]
+  float* lse2;              // [2 MAX_CTAS][128]
+  float* o;                 // [2 MAX_CTAS][128][D]
 };
+constexpr size_t REC_BYTES = 4096;
+static_assert(MAX_CTAS * sizeof(JoinRec) <= REC_BYTES, "join records");
 __host__ __device__ inline Scratch scratch_of(void* p) {
-  return {static_cast<float*>(p), static_cast<float*>(p) + MAX_PIECES * 128};
+  uint8_t* u = static_cast<uint8_t*>(p);
+  float* f = reinterpret_cast<float*>(u + REC_BYTES);
+  return {reinterpret_cast<JoinRec*>(u), f, f + 2 * MAX_CTAS * 128};
 }
 
 struct Args {
   CUtensorMap tk, tv;       // pages, boxes of `box` rows x 64 dims (tv: the pair kernel's)
   PagedAttnArgs a;
-  Grid grid;
+  int64_t n_slots;          // tile slots of the batch
   int box;                  // 16, 32 or 64, or 1: no TMA
 };
 
@@ -217,21 +230,17 @@ struct Args {
 template <int M>
 struct Item {
   int b, g, rows;           // sequence, KV head, rows in use
-  int n_tiles, tile0;       // tiles of this range, its first
-  int pieces, split;        // ranges that the item's keys are cut into, which one this is
+  int all, n_tiles, tile0;  // tiles; those of this CTA (n_tiles from tile0 on)
   int lo, ns, n_vis;        // key number v: v < ns ? v : lo + v - ns (whole boxes)
   int first, end;           // keys needed: [first, end) and those below the sinks
   int p0;                   // position of the first row's token
   int64_t t0, row0;         // the sequence's first token row; first flat row of the item
   __device__ __forceinline__ Item(const Args& x, int64_t w) {
     const PagedAttnArgs& a = x.a;
-    const int per = a.hq / a.hk, ns_ = x.grid.n_split;
-    n_tiles = 0;
-    tile0 = 0;
-    split = (int)(w % ns_);
-    w /= ns_;
+    const int per = a.hq / a.hk;
+    all = n_tiles = tile0 = 0;
     g = (int)(w % a.hk);
-    const int64_t slot = x.grid.n_slots - 1 - w / a.hk;
+    const int64_t slot = x.n_slots - 1 - w / a.hk;
     int l = 0, h = a.B;
     while (h - l > 1) {
       const int mid = (l + h) >> 1;
@@ -255,23 +264,106 @@ struct Item {
     n_vis = ns + end - lo;
     p0 = (int)min(pos, (int64_t)INT32_MAX);
     // at least one tile: rows whose keys all lie past the table come out zero
-    const int all = max((n_vis + KT - 1) / KT, 1), each = (all + ns_ - 1) / ns_;
-    pieces = (all + each - 1) / each;
-    tile0 = split * each;
-    n_tiles = min(each, all - tile0);
+    n_tiles = all = max((n_vis + KT - 1) / KT, 1);
+  }
+  // only tiles [from, to)
+  __device__ __forceinline__ void cut(int from, int to) {
+    tile0 = from;
+    n_tiles = min(all, to) - from;
   }
 };
 
-// The softmax warps (0-7): row r0 + r of an item of ROWS rows in TMEM lane r, items
-// w0, w0 + w_step, ..  In a pair of CTAs (PAIR) the MMA's barriers are the first
+// The items of a CTA (or pair): w, w + step, .. last; of the first the tiles from
+// `from` on, of the last those before `to`.
+struct Walk {
+  int64_t w, last, step;
+  int from, to;
+};
+template <int M, bool EVEN>
+__device__ __forceinline__ Item<M> item_of(const Args& x, const Walk& k, int64_t w) {
+  Item<M> it(x, w);
+  if (EVEN && it.n_tiles > 0) it.cut(w == k.w ? k.from : 0, w == k.last ? k.to : INT32_MAX);
+  return it;
+}
+// The same, through shuffles that tell the compiler that a warp has one walk.
+__device__ __forceinline__ Walk uniform(const Walk& k) {
+  auto one = [](auto v) { return __shfl_sync(0xffffffffu, v, 0); };
+  return {one(k.w), one(k.last), one(k.step), one(k.from), one(k.to)};
+}
+// All threads of a CTA, once: the walk of CTA (or pair) c of n over up to MAX_EVEN
+// items.  ITEM_COST units and a unit a tile for each, end to end, cut evenly, where
+// that is quicker than whole items in turn.  Each thread counts one item's; those
+// that hold the range's ends write them down.  buf: 2.5 KB of shared memory.
+template <int M>
+__device__ __forceinline__ Walk make_walk(const Args& x, int c, int n, void* buf) {
+  const int64_t n_items = x.n_slots * x.a.hk;
+  int64_t* sum = static_cast<int64_t*>(buf);                        // [16]
+  Walk* out = reinterpret_cast<Walk*>(sum + 16);
+  int32_t* item = reinterpret_cast<int32_t*>(out + 1);              // [MAX_EVEN]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Scratch sc = scratch_of(x.a.scratch);
+  const int tiles = tid < n_items ? Item<M>(x, tid).all : 0;
+  const int64_t units = tiles ? tiles + ITEM_COST : 0;
+  int64_t s = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += v;
+  }
+  if (lane == 31) sum[warp] = s;
+  item[tid] = (int32_t)units;
+  if (tid == 0) {
+    *out = {0, -1, 1, 0, 0};
+    sc.rec[c] = {0, -1};
+  }
+  __syncthreads();
+  // the longest walk of whole items
+  int64_t whole = 0;
+  if (tid < n)
+    for (int64_t i = tid; i < n_items; i += n) whole += item[i];
+  int64_t total = 0, at = s - units;                                // at: units before this item's
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) {
+    if (i < warp) at += sum[i];
+    total += sum[i];
+  }
+  // CTA c has the units from c base + min(c, more) on: base, or one more; CTAs
+  // beyond what is worth one have none
+  const int64_t parts = min((int64_t)n, max(total / LEAST, (int64_t)1));
+  const int64_t base = total / parts, more = total - base * parts;
+  if (!__syncthreads_or(whole > base + JOIN_COST)) return {c, n_items - 1, n, 0, INT32_MAX};
+  if (c < parts && units) {
+    const int64_t ua = c * base + min((int64_t)c, more), ub = ua + base + (c < more ? 1 : 0);
+    const int64_t tile0 = at + ITEM_COST, end = tile0 + tiles;      // the item's tiles
+    const int from = (int)max(ua - tile0, (int64_t)0), to = (int)max(min(ub, end) - tile0, (int64_t)0);
+    if (at <= ua && ua < end) {
+      out->w = tid;
+      out->from = from;
+    }
+    if (at < ub && ub <= end) {
+      out->last = tid;
+      out->to = to;
+    }
+    if (ua < end && ub > tile0 && from == 0 && to < tiles) {        // its first tile is here, its last is not
+      const int64_t u = end - 1;
+      sc.rec[c] = {tid, (int32_t)(u < more * (base + 1) ? u / (base + 1) : more + (u - more * (base + 1)) / base)};
+    }
+  }
+  __syncthreads();
+  return *out;
+}
+
+// The softmax warps (0-7): row r0 + r of an item of ROWS rows in TMEM lane r; cta:
+// number of the CTA (or pair).  In a pair of CTAs (PAIR) the MMA's barriers are the first
 // CTA's.
 struct SoftBars {
   uint64_t *s_full, *s_empty, *p_full, *pv_done, *hand, *turn, *xbar, *o_empty;
 };
-template <class E, int D, int ROWS, bool PAIR>
+template <class E, int D, int ROWS, bool PAIR, bool EVEN>
 __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint32_t off_ok, uint32_t off_xch, const SoftBars& bar,
-                                             uint32_t tmem, int warp, int lane, int r0, int64_t w0, int64_t w_step,
-                                             int64_t n_items, volatile int* abort_flag) {
+                                             uint32_t tmem, int warp, int lane, int r0, const Walk& walk, int64_t w_first, int64_t w_last,
+                                             int64_t w_step, int cta,
+                                             volatile int* abort_flag) {
   using X = Elem<E>;
   using TM = Tmem<D, PAIR>;
   const PagedAttnArgs& a = x.a;
@@ -286,14 +378,14 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, bar_wait<PAIR>(bar, parity, abort_flag, a.err));
   };
-  for (int64_t w = w0; ok && w < n_items; w += w_step) {
+  for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
     int n_tiles, v0;                                // tiles of the item, first key number of the tile
     int v_min, v_max;                               // the row sees v in [v_min, v_max] and v < sinks
     int all_min, all_max;                           // every row sees v in [all_min, all_max]
     int64_t orow;                                   // output row, or piece row; -1: row not in use
     bool part;
     {
-      const Item<ROWS> it(x, w);
+      const Item<ROWS> it = item_of<ROWS, EVEN>(x, walk, w);
       if (it.n_tiles <= 0) continue;
       n_tiles = it.n_tiles;
       v0 = it.tile0 * KT;
@@ -307,8 +399,8 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
       all_max = (int)min(pos_f + shift, (int64_t)it.n_vis - 1);
       v_min = a.window > 0 ? (int)max(pos - a.window + 1 + shift, (int64_t)0) : 0;
       all_min = a.window > 0 ? (int)max(pos1 - a.window + 1 + shift, (int64_t)0) : 0;
-      part = it.pieces > 1;
-      orow = !in ? -1 : part ? w * ROWS + r0 + r : (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
+      part = EVEN && it.n_tiles < it.all;
+      orow = !in ? -1 : part ? (int64_t)(2 * cta + (it.tile0 == 0 ? 1 : 0)) * ROWS + r0 + r : (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
     }
     float m = -FLT_MAX, l = 0.f;
     for (int i = (int)((count ^ wg) & 1); i < n_tiles; i += 2) {

@@ -37,7 +37,7 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <class E>
+template <class E, bool EVEN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_prefill_pair_kernel(const __grid_constant__ Args x) {
   constexpr uint32_t IDESC = umma_idesc_bf16_f32(M, KT) &
                              (std::is_same<E, __half>::value ? ~((1u << 7) | (1u << 10)) : ~0u);   // f16: 0
@@ -91,12 +91,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
   }
   pdl_launch();
   tc_fence_before();
+  // (without EVEN the walk is of launch constants, not through a structure that
+  // the roles' loops would have to read)
+  Walk walk{};
+  if constexpr (EVEN) walk = uniform(make_walk<M>(x, blockIdx.x >> 1, gridDim.x >> 1, smem));   // in Q's place
+  const int64_t w_first = EVEN ? walk.w : (int64_t)(blockIdx.x >> 1), w_step = EVEN ? walk.step : (int64_t)(gridDim.x >> 1);
+  const int64_t w_last = EVEN ? walk.last : x.n_slots * x.a.hk - 1;
   __syncthreads();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int64_t n_items = x.grid.n_slots * a.hk * x.grid.n_split;
-  const int64_t w0 = blockIdx.x >> 1, w_step = gridDim.x >> 1;
   const int per = a.hq / a.hk;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
@@ -110,8 +114,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
     // ---------------------------------------------------------------------- Q
     const int lt = tid - 32 * W_LOAD, c = lt & 7, rt = lt >> 3;
     uint32_t items_done = 0;
-    for (int64_t w = w0; w < n_items; w += w_step) {
-      const Item<M> it(x, w);
+    for (int64_t w = w_first; w <= w_last; w += w_step) {
+      const Item<M> it = item_of<M, EVEN>(x, walk, w);
       if (it.n_tiles <= 0) continue;
       // once the previous item's last S has read its own
       if (items_done > 0 && !wait(q_empty, (items_done - 1) & 1)) break;
@@ -137,8 +141,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
     uint32_t kph = 1, vph = 1, count = 0, k_used = 0, v_used = 0;   // used: stages that copies went to
     bool ok = true;
     const int box = x.box, nb = KT / box, nbk = nb / 2;            // boxes of a tile; of a K half
-    for (int64_t w = w0; ok && w < n_items; w += w_step) {
-      const Item<M> it(x, w);
+    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+      const Item<M> it = item_of<M, EVEN>(x, walk, w);
       if (it.n_tiles <= 0) continue;
       const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
       // lane i has box i of a tile (lanes past the last repeat): its page, or -1
@@ -217,8 +221,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
     uint32_t kph = 0, items_done = 0, count = 0;
     bool ok = true;
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
-    for (int64_t w = w0; ok && w < n_items; w += w_step) {
-      const Item<M> it(x, w);
+    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+      const Item<M> it = item_of<M, EVEN>(x, walk, w);
       const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
       if (n_tiles <= 0) continue;
       if (!wait(q_full, items_done & 1)) { ok = false; break; }
@@ -263,8 +267,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
     uint32_t vph = 0, items_done = 0, count = 0;
     bool ok = true;
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
-    for (int64_t w = w0; ok && w < n_items; w += w_step) {
-      const Item<M> it(x, w);
+    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+      const Item<M> it = item_of<M, EVEN>(x, walk, w);
       const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
       if (n_tiles <= 0) continue;
       for (int i = 0; i < n_tiles; ++i, ++count) {
@@ -309,8 +313,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
   } else if (warp < W_LOAD) {
     // ---------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
-    softmax_role<E, D, M, true>(x, smem, OFF_OK, OFF_XCH, {s_full, s_empty, p_full, pv_done, hand, turn, xbar, o_empty}, tmem, warp,
-                                lane, 128 * rank, w0, w_step, n_items, abort_flag);
+    softmax_role<E, D, M, true, EVEN>(x, smem, OFF_OK, OFF_XCH, {s_full, s_empty, p_full, pv_done, hand, turn, xbar, o_empty}, tmem, warp,
+                                lane, 128 * rank, walk, w_first, w_last, w_step, blockIdx.x >> 1, abort_flag);
   }
   tc_fence_before();
   __syncthreads();
@@ -321,35 +325,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
   }
 }
 
-template <class E>
+template <class E, bool EVEN>
 cudaError_t launch_pair(const Args& x, int grid, cudaStream_t s) {
   static bool attr_done[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr_done[dev]) {
-    e = cudaFuncSetAttribute(paged_prefill_pair_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+    e = cudaFuncSetAttribute(paged_prefill_pair_kernel<E, EVEN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev] = true;
   }
-  paged_prefill_pair_kernel<E><<<grid, THREADS, SMEM, s>>>(x);
+  paged_prefill_pair_kernel<E, EVEN><<<grid, THREADS, SMEM, s>>>(x);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_paged_prefill_pair(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int dtype,
-                                      int64_t n_slots, int n_split, int num_sms, cudaStream_t s) {
+                                      int64_t n_slots, int pairs, bool even, cudaStream_t s) {
   Args x;
   x.tk = tk;
   x.tv = tv;
   x.a = a;
-  x.grid.n_slots = n_slots;
-  x.grid.n_split = n_split;
+  x.n_slots = n_slots;
   x.box = paged_prefill_box(a.kv.page_size);
-  const int64_t items = n_slots * a.hk * n_split;
-  const int grid = 2 * (int)(items < num_sms / 2 ? items : num_sms / 2);
-  return dtype == QSA_DTYPE_BF16 ? launch_pair<__nv_bfloat16>(x, grid, s) : launch_pair<__half>(x, grid, s);
+  if (dtype == QSA_DTYPE_BF16)
+    return even ? launch_pair<__nv_bfloat16, true>(x, 2 * pairs, s) : launch_pair<__nv_bfloat16, false>(x, 2 * pairs, s);
+  return even ? launch_pair<__half, true>(x, 2 * pairs, s) : launch_pair<__half, false>(x, 2 * pairs, s);
 }
 
 }  // namespace qsa

@@ -188,6 +188,6 @@ int paged_prefill_box(int page_size);
 cudaError_t launch_paged_prefill(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
                                  int dtype, int num_sms, cudaStream_t s, bool join);
 cudaError_t launch_paged_prefill_pair(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int dtype,
-                                      int64_t n_slots, int n_split, int num_sms, cudaStream_t s);
+                                      int64_t n_slots, int pairs, bool even, cudaStream_t s);
 
 }  // namespace qsa
