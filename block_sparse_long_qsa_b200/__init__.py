@@ -549,6 +549,7 @@ INJECT_INDEXER_STALL = 1
 INJECT_ATTENTION_STALL = 2
 INJECT_ATTENTION_BAD_BLOCK = 3
 INJECT_ATTENTION_RESCALE_ALL = 4
+INJECT_PAGED_STALL = 5
 
 
 def qsa_debug_inject(code: int):

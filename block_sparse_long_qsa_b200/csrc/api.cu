@@ -935,7 +935,7 @@ int take_debug_injection(int code) {
 }  // namespace qsa
 
 extern "C" qsa_status qsa_debug_inject(int32_t code) {
-  if (code < QSA_INJECT_NONE || code > QSA_INJECT_ATTENTION_RESCALE_ALL) return QSA_ERR_INVALID_ARG;
+  if (code < QSA_INJECT_NONE || code > QSA_INJECT_PAGED_STALL) return QSA_ERR_INVALID_ARG;
   qsa::g_debug_inject.store(code);
   return QSA_OK;
 }
@@ -1253,8 +1253,10 @@ qsa_status qsa_norm_rope(const qsa_layer_params* p, int64_t T, int64_t pos0, con
                          void* q_out, void* k_out, void* stream) {
   qsa_status st = check_layer(p);
   if (st != QSA_OK) return st;
-  if (T < 0 || (!q != !q_out) || (!k != !k_out) || (!q && !k) || pos0 < 0) return QSA_ERR_INVALID_ARG;
+  if (T < 0 || pos0 < 0) return QSA_ERR_INVALID_ARG;
   if (T > INT32_MAX || pos0 > INT32_MAX) return QSA_ERR_UNSUPPORTED;
+  if (T == 0) return QSA_OK;                          // (arrays without an element may have no address)
+  if ((!q != !q_out) || (!k != !k_out) || (!q && !k)) return QSA_ERR_INVALID_ARG;
   if ((q && !stride_ok(q_ld, (int64_t)p->n_q_heads * p->head_dim)) ||
       (k && !stride_ok(k_ld, (int64_t)p->n_kv_heads * p->head_dim)))
     return QSA_ERR_INVALID_ARG;
@@ -1263,7 +1265,6 @@ qsa_status qsa_norm_rope(const qsa_layer_params* p, int64_t T, int64_t pos0, con
     return QSA_ERR_MISALIGNED;
   DevInfo di;
   if ((st = device_info(&di)) != QSA_OK) return st;
-  if (T == 0) return QSA_OK;
   qsa::NormRopeArgs a{};
   a.T = T; a.pos0 = pos0; a.positions = positions;
   a.q = static_cast<const uint16_t*>(q); a.q_ld = q_ld;
@@ -1298,8 +1299,10 @@ qsa_status qsa_paged_append(const qsa_layer_params* p, const qsa_paged_kv* kv, i
   if (st != QSA_OK) return st;
   qsa::NormRopeArgs a{};
   if ((st = check_kv(p, kv, B, &a.kv)) != QSA_OK) return st;
-  if (T < 0 || !cache_len || !k || !v || !ws || (!q != !q_out) || (!cu_new && T != B)) return QSA_ERR_INVALID_ARG;
+  if (T < 0 || (!cu_new && T != B)) return QSA_ERR_INVALID_ARG;
   if (T >= ((int64_t)1 << 24)) return QSA_ERR_UNSUPPORTED;
+  if (T == 0) return QSA_OK;
+  if (!cache_len || !k || !v || !ws || (!q != !q_out)) return QSA_ERR_INVALID_ARG;
   const int64_t kw = (int64_t)p->n_kv_heads * p->head_dim;
   if ((q && !stride_ok(q_ld, (int64_t)p->n_q_heads * p->head_dim)) || !stride_ok(k_ld, kw) || !stride_ok(v_ld, kw))
     return QSA_ERR_INVALID_ARG;
@@ -1309,7 +1312,6 @@ qsa_status qsa_paged_append(const qsa_layer_params* p, const qsa_paged_kv* kv, i
   if (ws_bytes < HEADER_BYTES) return QSA_ERR_WORKSPACE_TOO_SMALL;
   DevInfo di;
   if ((st = device_info(&di)) != QSA_OK) return st;
-  if (T == 0) return QSA_OK;
   a.T = T; a.positions = positions;
   a.q = static_cast<const uint16_t*>(q); a.q_ld = q_ld;
   a.k = static_cast<const uint16_t*>(k); a.k_ld = k_ld;
@@ -1365,13 +1367,14 @@ qsa_status qsa_paged_prefill(const qsa_layer_params* p, const qsa_paged_kv* kv, 
   if (st != QSA_OK) return st;
   qsa::PagedAttnArgs a{};
   if ((st = check_kv(p, kv, B, &a.kv)) != QSA_OK) return st;
-  if (T < 0 || !cu_new || !cache_len || !q || !out || !ws) return QSA_ERR_INVALID_ARG;
+  if (T < 0) return QSA_ERR_INVALID_ARG;
   if (T >= ((int64_t)1 << 24)) return QSA_ERR_UNSUPPORTED;
+  if (T == 0) return QSA_OK;
+  if (!cu_new || !cache_len || !q || !out || !ws) return QSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(ws)) return QSA_ERR_MISALIGNED;
   if (ws_bytes < paged_ws(p, B)) return QSA_ERR_WORKSPACE_TOO_SMALL;
   DevInfo di;
   if ((st = device_info(&di)) != QSA_OK) return st;
-  if (T == 0) return QSA_OK;
   a.B = B; a.hq = p->n_q_heads; a.hk = p->n_kv_heads; a.T = T;
   a.cu_new = cu_new;
   a.cache_len = cache_len;

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     fence_barrier_init();
   }
   if (warp == W_MMA) { tmem_alloc(tmem_slot, TMEM_COLS); tmem_relinquish(); }
-  pdl_launch();
+  if (EVEN) pdl_launch();                           // the join follows
   tc_fence_before();
   // (without EVEN the walk is of launch constants, not through a structure that
   // the roles' loops would have to read)
@@ -391,6 +391,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
           if (++kslot == NS) kslot = 0;
         }
         if (!ok) break;
+#ifdef QSA_DEBUG_HOOKS
+        // test hook: no CTA signals its first S, so the softmax times out
+        if (!(a.inject == QSA_INJECT_PAGED_STALL && count == 0))
+#endif
         umma_commit(&s_full[count & 1]);
         if (i == n_tiles - 1) umma_commit(q_empty);
       }
@@ -538,11 +542,13 @@ cudaError_t launch_attn(const Args& x, int grid, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr_done[dev]) {
-    e = cudaFuncSetAttribute(paged_prefill_kernel<E, D, TMA, EVEN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+    e = prepare_launch(paged_prefill_kernel<E, D, TMA, EVEN>, SMEM);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev] = true;
   }
-  paged_prefill_kernel<E, D, TMA, EVEN><<<grid, THREADS, SMEM, s>>>(x);
+  Args y = x;
+  y.a.inject = take_debug_injection(QSA_INJECT_PAGED_STALL);
+  paged_prefill_kernel<E, D, TMA, EVEN><<<grid, THREADS, SMEM, s>>>(y);
   return cudaGetLastError();
 }
 

@@ -39,6 +39,16 @@ constexpr int MAX_EVEN = THREADS;                   // most items that may be cu
 // tiles in a row, cut 15 and 50 us; 16 x 30 tokens over 1000 keys: whole 14 and 29
 // us, cut 10 and 50 us.)
 constexpr int ITEM_COST = 6, LEAST = 4, JOIN_COST = 15;
+// setmaxnreg.inc takes from what the launch allotted: the kernel must have been
+// compiled to the registers that the split adds up to, or it would wait for ever.
+template <class F>
+cudaError_t prepare_launch(F* kernel, uint32_t smem) {
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs * THREADS < 256 * (REGS_SOFT + REGS_REST)) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
 // Quarter of a tile's exponentials after which the next tile's begin (32K tokens
 // of 24 + 2 heads of 256: 9.65 ms with 1, 9.85 with 2, 9.87 without turns; 16K of
 // 16 heads of 64: 1.20 ms with 1, 1.19 with 2, 1.27 without; 128: 3.0 ms with 1,

@@ -89,7 +89,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  pdl_launch();
+  if (EVEN) pdl_launch();                           // the join follows
   tc_fence_before();
   // (without EVEN the walk is of launch constants, not through a structure that
   // the roles' loops would have to read)
@@ -250,6 +250,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
             umma_ss<2>(tm + TM::s(0), desc_at(DESC_K, base + (e >> 2) * 16384 + 32 * (e & 3)),
                        desc_at(DESC_K, kb + (e >> 2) * 8192 + 32 * (e & 3)), IDESC, e > 0 ? 1u : 0u);
           umma_commit<2>(&k_empty[ks]);
+#ifdef QSA_DEBUG_HOOKS
+          // test hook: no pair signals its first S, so the softmax times out
+          if (!(a.inject == QSA_INJECT_PAGED_STALL && count == 0))
+#endif
           umma_commit<2>(&s_full[count & 1]);
           if (i == n_tiles - 1) umma_commit<2>(q_empty);
         }
@@ -332,11 +336,13 @@ cudaError_t launch_pair(const Args& x, int grid, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr_done[dev]) {
-    e = cudaFuncSetAttribute(paged_prefill_pair_kernel<E, EVEN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+    e = prepare_launch(paged_prefill_pair_kernel<E, EVEN>, SMEM);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev] = true;
   }
-  paged_prefill_pair_kernel<E, EVEN><<<grid, THREADS, SMEM, s>>>(x);
+  Args y = x;
+  y.a.inject = take_debug_injection(QSA_INJECT_PAGED_STALL);
+  paged_prefill_pair_kernel<E, EVEN><<<grid, THREADS, SMEM, s>>>(y);
   return cudaGetLastError();
 }
 

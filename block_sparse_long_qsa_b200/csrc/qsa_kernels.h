@@ -175,6 +175,7 @@ struct PagedAttnArgs {
   int window, sinks;
   uint32_t* err;
   void* scratch;            // behind the workspace's header
+  int inject;               // debug build: fault-injection code (QSA_INJECT_*), else 0
 };
 size_t paged_decode_scratch(int head_dim, int B);
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, int head_dim, int dtype, int num_sms, cudaStream_t s,

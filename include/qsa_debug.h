@@ -37,6 +37,7 @@ enum {
   QSA_INJECT_INDEXER_STALL = 1,        /* next indexer launch: CTA 0 never signals its first accumulator */
   QSA_INJECT_ATTENTION_STALL = 2,      /* next prefill attention launch: CTA 0 never signals its first S tile */
   QSA_INJECT_ATTENTION_BAD_BLOCK = 3,  /* next prefill attention launch: CTA 0's first gathered block is qb + 1 */
+  QSA_INJECT_PAGED_STALL = 5,          /* next qsa_paged_prefill: no CTA signals its first S tile */
   QSA_INJECT_ATTENTION_RESCALE_ALL = 4 /* next attention launch (prefill or decode): the online softmax takes a
                                           new running maximum, and rescales the accumulated output, on every tile
                                           (no lazy margin), so that path runs on ordinary inputs */

@@ -44,6 +44,37 @@ def test_norm_rope(heads, rope, dt, T):
         U.check_norm_rope(got, *U.norm_rope64(p, x, w, pos), dt)
 
 
+def test_norm_rope_and_append_of_many_tokens():
+    """Enough tokens for a warp a token, ragged."""
+    T, hq, hk, D, page = 3300, 6, 2, 128, 16
+    p = qsa.layer_params(hq, hk, D)
+    g = gen(13)
+    qkv = randn(g, BF, T, hq + 2 * hk, D)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+    qw, kw = randn(g, BF, D), randn(g, BF, D)
+    qo, ko = torch.empty(T, hq, D, dtype=BF, device="cuda"), torch.empty(T, hk, D, dtype=BF, device="cuda")
+    qsa.qsa_norm_rope(p, T, 5, q, k, qw, kw, qo, ko)
+    pos = 5 + torch.arange(T, device="cuda")[None]
+    U.check_norm_rope(qo, *U.norm_rope64(p, q, qw, pos), BF)
+    U.check_norm_rope(ko, *U.norm_rope64(p, k, kw, pos), BF)
+    cached, new = [5, 0, -1, 900], [1000, 1, 299, 1990]
+    cache = U.Cache(p, [max(c, 0) + n for c, n in zip(cached, new)], page, BF, "cuda", "head")
+    cu = torch.tensor([0, 1000, 1001, 1300, 3290], dtype=torch.int32, device="cuda")
+    cl = torch.tensor(cached, dtype=torch.int32, device="cuda")
+    ws = qsa.paged_workspace(p, 4, T)
+    qo.fill_(5)
+    qsa.qsa_paged_append(p, cache.kv, 4, T, cu, cl, k, v, ws, q=q, q_out=qo, q_weight=qw, k_weight=kw)
+    assert ok(ws) == 0
+    for b in (0, 1, 3):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        at = cached[b] + torch.arange(new[b], device="cuda")
+        pg, sl = cache.slots(b, at)
+        U.check_norm_rope(qo[rows], *U.norm_rope64(p, q[rows], qw, at[None]), BF)
+        U.check_norm_rope(cache.k[pg, sl], *U.norm_rope64(p, k[rows], kw, at[None]), BF)
+        assert torch.equal(cache.v[pg, sl], v[rows])
+    assert bool((qo[1001:1300] == 5).all()) and bool((qo[3290:] == 5).all())
+
+
 @pytest.mark.parametrize("rope,section", [(64, (11, 11, 10)), (64, (16, 8, 8)), (128, (24, 20, 20)), (32, (16, 0, 0)), (64, (21, 0, 11)), (128, (22, 22, 20))])
 @pytest.mark.parametrize("interleaved", [0, 1])
 def test_three_axes(rope, section, interleaved):
@@ -441,6 +472,136 @@ def test_prefill_of_one_token_each_is_a_decode():
     assert float((a.double() - b.double()).abs().max()) < 2e-2 and float((la - lb).abs().max()) < 1e-4
 
 
+@pytest.mark.parametrize("heads,cached,new", [
+    ((24, 2, 256), [5000], [600]),                      # pairs of CTAs, tiles cut over them
+    ((24, 2, 256), [0, 777], [3001, 40]),               # pairs, whole items
+    ((24, 2, 256), [3000, 0, 20, 9001], [9, 1, 4, 2]),  # single CTAs, cut: few rows
+    ((28, 4, 128), [0], [2501]),                        # single CTAs, whole items
+    ((28, 4, 128), [4000, 0], [30, 300]),
+    ((16, 16, 64), [100], [1300]),
+    ((16, 16, 64), [8000], [3]),
+    ((64, 1, 128), [33], [700])])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 5)])
+def test_prefill_ways_to_deal_the_tiles(heads, cached, new, window, sinks):
+    """Each kernel and each way to deal the tiles to the CTAs, twice with the same bits."""
+    p = qsa.layer_params(*heads, window=window, n_sinks=sinks)
+    cache, q, cl, cu = batch(p, cached, new, 32, BF, seed=len(new))
+    out, lse, ws = run_prefill(p, cache, q, cl, cu)
+    assert ok(ws) == 0
+    check_batch(p, cache, cached, new, q, out, lse, BF, some)
+    again, lse2, _ = run_prefill(p, cache, q, cl, cu, ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("heads", [(24, 2, 256), (28, 4, 128)])
+def test_window_past_the_table_leaves_zero_rows(heads):
+    """Rows whose keys all lie past the table: zero, lse -inf, reported."""
+    p = qsa.layer_params(*heads, window=8)
+    cache, q, cl, cu = batch(p, [40], [4], 16, BF)
+    far = torch.tensor([4096], dtype=torch.int32, device="cuda")
+    out, lse, ws = run_prefill(p, cache, q, far, cu)
+    assert ok(ws) == 7
+    assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
+    out, lse, ws = run_decode(p, cache, q[:1].contiguous(), far, ws)
+    assert ok(ws) == 7
+    assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
+
+
+def test_prefill_captured_follows_lengths():
+    """A graph of append and prefill replayed with other lengths, offsets and pages."""
+    hq, hk, D, B, T = 24, 2, 256, 3, 64
+    p = qsa.layer_params(hq, hk, D)
+    g = gen(3)
+    cache = U.Cache(p, [500] * B, 16, BF, "cuda")
+    for b in range(B):
+        cache.fill(b, 0, 500, randn(g, BF, 500, hk, D), randn(g, BF, 500, hk, D))
+    cl = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    q, k, v = randn(g, BF, T, hq, D), randn(g, BF, T, hk, D), randn(g, BF, T, hk, D)
+    qo, out, lse = torch.zeros_like(q), torch.zeros_like(q), torch.zeros(T, hq, device="cuda")
+    ws = qsa.paged_workspace(p, B, T)
+
+    def step():
+        qsa.qsa_paged_append(p, cache.kv, B, T, cu, cl, k, v, ws, q=q, q_out=qo)
+        qsa.qsa_paged_prefill(p, cache.kv, B, T, cu, cl, qo, out, ws, lse=lse)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                                          # warm up on nothing
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for cached, new in (([0, 300, 17], [30, 1, 33]), ([400, -1, 0], [5, 20, 0]), ([1, 2, 3], [64, 0, 0])):
+        for t in (q, k, v):
+            t.copy_(randn(g, BF, *t.shape))
+        out.fill_(9)
+        cl.copy_(torch.tensor(cached))
+        cu.copy_(torch.tensor([0] + list(torch.tensor(new).cumsum(0))))
+        graph.replay()
+        check_batch(p, cache, cached, new, qo, out, lse, BF)
+        assert bool((out[sum(new):] == 9).all())
+    assert ok(ws) == 0
+
+
+def test_two_streams_with_a_workspace_each():
+    """A decode and a prefill at the same time give what they give alone."""
+    p = qsa.layer_params(24, 2, 256)
+    cached, new = [3000, 700, 20], [50, 9, 300]
+    cache, q, cl, cu = batch(p, cached, new, 16, BF)
+    d_cache, d_q, d_cl, _ = batch(p, [9000, 100, 2000, 5] * 8, [1] * 32, 16, BF, seed=5)
+    want, want_l, ws1 = run_prefill(p, cache, q, cl, cu)
+    d_want, d_want_l, ws2 = run_decode(p, d_cache, d_q, d_cl)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        out, lse, d_out, d_lse = (torch.zeros_like(x) for x in (want, want_l, d_want, d_want_l))
+        torch.cuda.synchronize()
+        qsa.qsa_paged_prefill(p, cache.kv, 3, q.shape[0], cu, cl, q, out, ws1, lse=lse, stream=s1)
+        qsa.qsa_paged_decode(p, d_cache.kv, 32, d_cl, d_q, d_out, ws2, lse=d_lse, stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_l)
+        assert torch.equal(d_out, d_want) and torch.equal(d_lse, d_want_l)
+    assert ok(ws1) == 0 and ok(ws2) == 0
+
+
+def test_shared_pages():
+    """Sequences that share the pages of a common prefix."""
+    p = qsa.layer_params(24, 2, 256)
+    cached, new = [200, 200], [3, 40]
+    cache, q, cl, cu = batch(p, cached, new, 16, BF)
+    cache.table[1, :12] = cache.table[0, :12]           # 192 tokens in common
+    out, lse, ws = run_prefill(p, cache, q, cl, cu)
+    check_batch(p, cache, cached, new, q, out, lse, BF)
+    out, lse, ws = run_decode(p, cache, q[:2].contiguous(), cl, ws)
+    check_batch(p, cache, cached, [1, 1], q[:2], out, lse, BF)
+    assert ok(ws) == 0
+
+
+@pytest.mark.parametrize("heads", [(24, 2, 256), (28, 4, 128)])
+@pytest.mark.parametrize("new", [[5], [400]])
+def test_wait_that_runs_out_is_reported(heads, new):
+    """Debug build: no CTA signals its first tile of scores; the waits run
+    out (20 ms), the call ends with QSA_ERR_DEVICE_TIMEOUT, and the next is right."""
+    from block_sparse_long_qsa_b200 import _build
+    _build.build(debug=True)
+    p = qsa.layer_params(*heads)
+    cache, q, cl, cu = batch(p, [300], new, 64, BF)
+    want, want_l, ws = run_prefill(p, cache, q, cl, cu)
+    assert ok(ws) == 0
+    prev = qsa.use_library(qsa.LIB_DEBUG_PATH)
+    try:
+        qsa.qsa_debug_inject(qsa.INJECT_PAGED_STALL)
+        run_prefill(p, cache, q, cl, cu, ws)
+        assert ok(ws) == 6
+        out, lse, _ = run_prefill(p, cache, q, cl, cu, ws)
+        assert ok(ws) == 0
+        assert torch.equal(out, want) and torch.equal(lse, want_l)
+    finally:
+        qsa.use_library(prev or qsa.LIB_PATH)
+
+
 # ---------------------------------------------------------------- a run of them
 def test_dense_layer_equals_qsa_prefill():
     """While the budget covers every block, QSA is dense causal attention: the
@@ -479,6 +640,9 @@ def test_norms_feed_qsa_prefill():
     qr, _ = U.norm_rope64(p, qkv[:, :24], qw, pos)
     kr, _ = U.norm_rope64(p, qkv[:, 24:26], kw, pos)
     torch.cuda.synchronize()
+    # The calls round the normed and the rotated operands (two half steps of 2^-8
+    # each for q and k): scores of about 1 move by 2^-6, outputs of about 1 by that
+    # times their spread, and one rounding: below 3e-2.
     for i in (0, 1, 7, 250, 499):
         want, *_ = U.attend64(p, qr[i], kr[:i + 1], qkv[:i + 1, 26:].double())
         assert float((r["out"][i].view(BF).double() - want).abs().max()) < 3e-2
@@ -529,7 +693,8 @@ def test_serving_run(window, sinks):
     assert ok(ws) == 0
     for b in range(B):
         x = qkv[b]
-        # the rounded queries and keys that the calls hand on
+        # the rounded queries and keys that the calls hand on (where a value lies on
+        # a border of rounding they may differ by a step, 2^-7: as above)
         qr = U.norm_rope64(p, x[:, :hq], qw, pos[b])[0].to(BF)
         kr = U.norm_rope64(p, x[:, hq:hq + hk], kw, pos[b])[0].to(BF).double()
         for i in {0, 4, 49, 50, total[b] - steps - 1, total[b] - steps, total[b] - 1}:
