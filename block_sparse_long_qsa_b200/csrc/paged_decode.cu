@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
       if (i + 1 < n_units) issue();                // the last one's slot serves the merge first
     }
 
-    // ---- merge of the four warps' rows, each through the slot it used last
+    // ---- merge of the warps' rows, each through the slot it used last
 #pragma unroll
     for (int d = 1; d <= 2; d <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, d);
@@ -417,36 +417,43 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
     const int64_t item0 = x - ca.u;                // the item's first unit
     // pieces of an item: 2c + 1 where it starts in CTA c, 2c where it came in from before
     const int piece = 2 * blockIdx.x + (item0 >= ua ? 1 : 0);
-    for (int e = tid; e < rows * (D / 4); e += THREADS) {
-      const int r = e / (D / 4), c = 4 * (e % (D / 4));
-      float mx = -INFINITY;
+    if (tid < rows) {                              // each warp's share of a row, and the row's log-sum-exp
+      float mx = -INFINITY, l = 0.f, f[WARPS];
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, ml[w * ROWS + r].x);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float l = 0.f;
+      for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, ml[w * ROWS + tid].x);
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
-        const float2 s = ml[w * ROWS + r];
-        const float f = s.x == -INFINITY ? (s.y == 0.f ? 0.f : 1.f) : exp2_approx(s.x - mx);
+        const float2 s = ml[w * ROWS + tid];
+        f[w] = s.x == -INFINITY ? (s.y == 0.f ? 0.f : 1.f) : exp2_approx(s.x - mx);
+        l = fmaf(f[w], s.y, l);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // no key at all: zero
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) ml[w * ROWS + tid].x = f[w] * inv;
+      const float lse2 = l == 0.f ? -INFINITY : mx + log2f(l);
+      if (!whole) sc.lse2[piece * ROWS + tid] = lse2;
+      else if (a.lse) a.lse[qrow + tid] = lse2 * 0.69314718055994531f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ROWS * (D / 4) / THREADS; ++i) {
+      const int e = i * THREADS + tid, r = e / (D / 4), c = 4 * (e % (D / 4));
+      if (r >= rows) break;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = ml[w * ROWS + r].x;
         const float4 v = *reinterpret_cast<const float4*>(smem + (w * STAGES + last_slot) * SLOT +
                                                           (r * D + (c ^ ((r & 7) << 3))) * 4);
-        l = fmaf(f, s.y, l);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
         acc.z = fmaf(f, v.z, acc.z);
         acc.w = fmaf(f, v.w, acc.w);
       }
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // no key at all: zero
-      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-      const float lse2 = l == 0.f ? -INFINITY : mx + log2f(l);
-      if (whole) {
-        uint2 res = make_uint2(X::pack(acc.x, acc.y), X::pack(acc.z, acc.w));
-        *reinterpret_cast<uint2*>(a.out + (qrow + r) * D + c) = res;
-        if (c == 0 && a.lse) a.lse[qrow + r] = lse2 * 0.69314718055994531f;
-      } else {
+      if (whole)
+        *reinterpret_cast<uint2*>(a.out + (qrow + r) * D + c) = make_uint2(X::pack(acc.x, acc.y), X::pack(acc.z, acc.w));
+      else
         *reinterpret_cast<float4*>(sc.o + ((int64_t)piece * ROWS + r) * D + c) = acc;
-        if (c == 0) sc.lse2[piece * ROWS + r] = lse2;
-      }
     }
     if (!whole && item0 >= ua && tid == 0)
     {

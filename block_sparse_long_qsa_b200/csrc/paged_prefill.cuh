@@ -449,6 +449,7 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
           const int vq = vt + 32 * q;
           const uint32_t mask = (squeeze(bits[2 * q]) | squeeze(bits[2 * q + 1]) << 16) & below(v_max + 1 - vq) &
                                 (~below(v_min - vq) | below(a.sinks - vq));
+          if (__all_sync(0xffffffffu, mask == ~0u)) continue;       // most quarters of a border tile
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!(mask >> e & 1)) s[q][e] = -INFINITY;
@@ -558,11 +559,13 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
     const float inv = lr == 0.f ? 0.f : 1.f / lr;   // no key at all: zero
     const float lse2 = lr == 0.f ? -INFINITY : m + log2f(lr);
     const Scratch sc = scratch_of(a.scratch);
-#pragma unroll 1
+    float ov[D / 64][32];                            // all loads at once
+#pragma unroll
+    for (int cc = 0; cc < D / 64; ++cc) tmem_ld32(tmem + lanes + TM::O + (D / 2) * wg + 32 * cc, ov[cc]);
+#pragma unroll
     for (int cc = 0; cc < D / 64; ++cc) {
-      float o[32];
+      float (&o)[32] = ov[cc];
       const int d0 = (D / 2) * wg + 32 * cc;
-      tmem_ld32(tmem + lanes + TM::O + d0, o);
       tmem_ld_wait(o);
       if (orow >= 0 && part) {
         float4* dst = reinterpret_cast<float4*>(sc.o + orow * D + d0);
