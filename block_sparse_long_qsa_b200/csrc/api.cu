@@ -1215,6 +1215,10 @@ size_t paged_ws(const qsa_layer_params* p, int32_t B) {
          align_up(std::max(qsa::paged_decode_scratch(p->head_dim, B), qsa::paged_prefill_scratch(p->head_dim)));
 }
 
+// No position is beyond 2^30: more sinks mean the same, and the kernels round them
+// up to whole boxes in 32 bits.
+int32_t layer_sinks(const qsa_layer_params* p) { return std::min(p->n_sinks, (int32_t)1 << 30); }
+
 float layer_scale_log2(const qsa_layer_params* p) {
   const float s = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)p->head_dim);
   return s * 1.4426950408889634f;
@@ -1347,7 +1351,7 @@ qsa_status qsa_paged_decode(const qsa_layer_params* p, const qsa_paged_kv* kv, i
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.scale_log2 = layer_scale_log2(p);
-  a.window = p->window; a.sinks = p->n_sinks;
+  a.window = p->window; a.sinks = layer_sinks(p);
   a.err = static_cast<uint32_t*>(ws);
   a.scratch = static_cast<uint8_t*>(ws) + HEADER_BYTES;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1382,7 +1386,7 @@ qsa_status qsa_paged_prefill(const qsa_layer_params* p, const qsa_paged_kv* kv, 
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.scale_log2 = layer_scale_log2(p);
-  a.window = p->window; a.sinks = p->n_sinks;
+  a.window = p->window; a.sinks = layer_sinks(p);
   a.err = static_cast<uint32_t*>(ws);
   a.scratch = static_cast<uint8_t*>(ws) + HEADER_BYTES;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

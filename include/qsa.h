@@ -498,10 +498,11 @@ qsa_status qsa_paged_decode(const qsa_layer_params* p, const qsa_paged_kv* kv, i
 /* Attention of T new tokens of B sequences (ragged, cu_new) over their pages:
  * every token sees the keys up to its own position that window and sinks leave,
  * cached ones and the call's own (already appended).  q, out
- * [T][n_q_heads][head_dim], lse [T][n_q_heads] (nullable).  What the pages hold
- * behind a sequence's last token is not read; a V row that is not finite
- * reaches only the tokens that see it and, within its tile of 128 keys, may turn
- * rows of earlier tokens of the same call into NaN.  B <= 4096, T < 2^24. */
+ * [T][n_q_heads][head_dim], lse [T][n_q_heads] (nullable).  Rows of the
+ * pages behind a sequence's last token and those that no token of the call sees
+ * may hold anything, and so may a K row for the tokens that do not see it.  A V
+ * row that is not finite reaches the tokens that see it and may turn other rows
+ * of the same call, those whose tile of 128 keys it is in, into NaN.  B <= 4096, T < 2^24. */
 qsa_status qsa_paged_prefill(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B, int64_t T,
                              const int32_t* cu_new, const int32_t* cache_len, const void* q, void* out, float* lse,
                              void* ws, size_t ws_bytes, void* stream);

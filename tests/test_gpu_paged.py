@@ -413,13 +413,72 @@ def test_prefill(heads, dt, page, layout):
 def test_prefill_window(heads, window, sinks):
     p = qsa.layer_params(*heads, window=window, n_sinks=sinks)
     cached, new = [0, 2 * window + 77, window, 0], [300, 130, 1, 2 * window + 9 if window < 500 else 3]
-    g = gen(window)
     cache, q, cl, cu = batch(p, cached, new, 16, BF, seed=window)
-    # a token in the middle of a chunk may see more than the ends: every page from the first window on is there
     out, lse, ws = run_prefill(p, cache, q, cl, cu)
     assert ok(ws) == 0
     check_batch(p, cache, cached, new, q, out, lse, BF, some)
-    assert g is not None
+
+
+@pytest.mark.parametrize("heads", [(24, 2, 256), (28, 4, 128)])
+@pytest.mark.parametrize("window,sinks", [(100, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 0)])
+def test_window_and_sinks_of_any_size(heads, window, sinks):
+    """The largest windows and sinks leave every key."""
+    p = qsa.layer_params(*heads, window=window, n_sinks=sinks)
+    cached, new = [700, 0, 130], [5, 300, 1]
+    cache, q, cl, cu = batch(qsa.layer_params(*heads), cached, new, 64, BF)
+    out, lse, ws = run_prefill(p, cache, q, cl, cu)
+    assert ok(ws) == 0
+    check_batch(qsa.layer_params(*heads), cache, cached, new, q, out, lse, BF, some)
+    out, lse, ws = run_decode(p, cache, q[:3].contiguous(), cl, ws)
+    assert ok(ws) == 0
+    check_batch(qsa.layer_params(*heads), cache, cached, [1] * 3, q[:3], out, lse, BF)
+
+
+@pytest.mark.parametrize("heads", [(24, 2, 256), (28, 4, 128)])
+def test_offsets_past_the_tokens(heads):
+    """Offsets beyond T count as T: nothing behind row T is read or written."""
+    p = qsa.layer_params(*heads, rope_dim=0)
+    hq, hk, D = heads
+    cached, new = [40, 0], [30, 50]
+    cache, q, cl, cu = batch(p, cached, new, 16, BF)
+    wide = cu.clone()
+    wide[2] = 5000
+    out = torch.full((100, hq, D), 9.0, dtype=BF, device="cuda")
+    lse = torch.full((100, hq), 9.0, device="cuda")
+    ws = qsa.paged_workspace(p, 2, 80)
+    k, v = (cache.rows(1, torch.arange(50).cuda())[i].to(BF) for i in (0, 1))
+    k, v = (torch.cat([torch.zeros(30, hk, D, dtype=BF, device="cuda"), x]) for x in (k, v))
+    cl2 = torch.tensor([-1, 0], dtype=torch.int32, device="cuda")
+    qsa.qsa_paged_append(p, cache.kv, 2, 80, wide, cl2, k, v, ws)
+    qsa.qsa_paged_prefill(p, cache.kv, 2, 80, wide, cl, q, out, ws, lse=lse)
+    assert ok(ws) == 0
+    check_batch(p, cache, cached, new, q, out, lse, BF)
+    assert bool((out[80:] == 9).all()) and bool((lse[80:] == 9).all())
+
+
+def test_two_graphs_with_one_workspace():
+    """Graphs of a chunk cut over the CTAs and of a decode that share a workspace, replayed in turn."""
+    p = qsa.layer_params(24, 2, 256)
+    cache, q, cl, cu = batch(p, [9000, 20], [9, 40], 16, BF)
+    d_cache, d_q, d_cl, _ = batch(p, [5000, 3, 800], [1] * 3, 16, BF, seed=5)
+    ws = qsa.paged_workspace(p, 3, q.shape[0])
+    want, want_l, _ = run_prefill(p, cache, q, cl, cu, ws)
+    d_want, d_want_l, _ = run_decode(p, d_cache, d_q, d_cl, ws)
+    check_batch(p, cache, [9000, 20], [9, 40], q, want, want_l, BF)
+    out, lse, d_out, d_lse = (torch.zeros_like(x) for x in (want, want_l, d_want, d_want_l))
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    with torch.cuda.graph(graphs[0]):
+        qsa.qsa_paged_prefill(p, cache.kv, 2, q.shape[0], cu, cl, q, out, ws, lse=lse)
+    with torch.cuda.graph(graphs[1]):
+        qsa.qsa_paged_decode(p, d_cache.kv, 3, d_cl, d_q, d_out, ws, lse=d_lse)
+    for i in (0, 1, 1, 0, 0, 1):
+        for t in (out, lse, d_out, d_lse):
+            t.zero_()
+        graphs[i].replay()
+        graphs[1 - i].replay()
+        assert torch.equal(out, want) and torch.equal(lse, want_l)
+        assert torch.equal(d_out, d_want) and torch.equal(d_lse, d_want_l)
+    assert ok(ws) == 0
 
 
 def test_prefill_long_prefix_few_rows():
