@@ -51,6 +51,13 @@ template <> struct Elem<__half> {
   }
 };
 
+// x / y for 0 <= x, 0 < y: in 32 bits where both fit (a 64-bit division is a
+// routine of about a hundred instructions).
+__device__ __forceinline__ int64_t div64(int64_t x, int64_t y) {
+  if (((uint64_t)(x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+  return x / y;
+}
+
 // ------------------------------------------------------------- page tables --
 // j / page_size for 0 <= j < 2^31 by a multiplication (round-up method of
 // Granlund and Montgomery; the constants are made on the host).

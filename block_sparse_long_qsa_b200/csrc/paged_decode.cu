@@ -84,13 +84,6 @@ struct Visible {
   __device__ __forceinline__ int key(int v) const { return v < ns ? v : lo + (v - ns); }
 };
 
-// x / y for 0 <= x, 0 < y: in 32 bits where both fit (a 64-bit division is a
-// routine of about a hundred instructions).
-__device__ __forceinline__ int64_t div64(int64_t x, int64_t y) {
-  if (((uint64_t)(x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
-  return x / y;
-}
-
 template <class E, int D>
 __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int WARPS = warps_of(D), THREADS = 32 * WARPS;

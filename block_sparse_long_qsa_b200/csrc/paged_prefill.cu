@@ -46,11 +46,13 @@ namespace qsa {
 namespace {
 
 constexpr int M = 128;                              // query rows of an item
-// Query rows of a sequence, on average, from which pairs are used (24 + 2 heads of
-// 256, single against pairs: one of 37 tokens, 444 rows, over 20K keys 67 against
-// 79 us whole and uncut; 16 of 30 tokens, 360 rows, 29 against 63; 16 of 100, 1200
-// rows, 86 against 72; one of 2000 tokens 87 against 70).
-constexpr int64_t PAIR_ROWS = 512;
+// Query rows of a sequence, on average, from which pairs are used: more than one
+// tile of 128 (24 + 2 heads of 256, single against pairs: 11 tokens, 132 rows, over
+// 80K keys 75 and 64 us; 21 tokens 78 and 71; 37 tokens 110 and 95; 8 x 37 over 20K
+// 215 and 173; 16 x 30 over 1000 37 and 35; but 10 tokens, 120 rows, over 20K 32.5
+// and 34.8).
+constexpr int64_t PAIR_ROWS = 129;
+constexpr int JOIN_CTAS = 592;                      // of the join: four to an SM
 constexpr uint32_t SLOT = 16384;
 constexpr int NS = 5;                               // slots of the K ring and of the V ring
 constexpr uint32_t OFF_K = 65536;                   // Q: up to 128 rows x 512 B
@@ -122,12 +124,12 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   // the roles' loops would have to read)
   Walk walk{};
   if constexpr (EVEN) walk = uniform(make_walk<M>(x, blockIdx.x, gridDim.x, smem));   // in Q's place
-  const int64_t w_first = EVEN ? walk.w : (int64_t)blockIdx.x, w_step = EVEN ? walk.step : (int64_t)gridDim.x;
-  const int64_t w_last = EVEN ? walk.last : x.n_slots * x.a.hk - 1;
+  const ItemNo<EVEN> w_first = EVEN ? walk.w : blockIdx.x, w_step = EVEN ? walk.step : gridDim.x;
+  const ItemNo<EVEN> w_last = EVEN ? walk.last : x.n_slots * x.a.hk - 1;
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int per = a.hq / a.hk;
+  const uint32_t per = (uint32_t)a.hq / (uint32_t)a.hk;
 
   if (warp >= W_LOAD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
   if (warp >= W_LOAD && warp < W_MMA) {
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+    for (ItemNo<EVEN> w = w_first; ok && w <= w_last; w += w_step) {
       const Item<M> it = item_of<M, EVEN>(x, walk, w);
       if (it.n_tiles <= 0) continue;
       const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
@@ -260,8 +262,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
         for (int j = 0; j < RJ; ++j) {
           const int r = RT * j + rt;
           const bool valid = r < it.rows;
-          const int64_t f = it.row0 + (valid ? r : 0);
-          const uint16_t* src = a.q + ((it.t0 + f / per) * a.hq + it.g * per + f % per) * D + 8 * c;
+          const uint32_t f = it.row0 + (valid ? r : 0);
+          const uint16_t* src = a.q + it.q_row(a, per, f) * D + 8 * c;
 #pragma unroll
           for (int ch = 0; ch < NCH; ++ch)
             cp_async16_zfill(smem_u32(smem + ch * SLOT) + swz128(r, c), valid ? src + 64 * ch : a.q, valid);
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     uint32_t landing = 0, open = 0;                // groups that copies went to; arrivals of an unfinished one
     bool ok = true;
     const int box = x.box, nb = KT / box;
-    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+    for (ItemNo<EVEN> w = w_first; ok && w <= w_last; w += w_step) {
       const Item<M> it = item_of<M, EVEN>(x, walk, w);
       if (it.n_tiles <= 0) continue;
       const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
     };
-    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+    for (ItemNo<EVEN> w = w_first; ok && w <= w_last; w += w_step) {
       const Item<M> it = item_of<M, EVEN>(x, walk, w);
       const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
       if (n_tiles <= 0) continue;
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
     };
-    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+    for (ItemNo<EVEN> w = w_first; ok && w <= w_last; w += w_step) {
       const Item<M> it = item_of<M, EVEN>(x, walk, w);
       const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
       if (n_tiles <= 0) continue;
@@ -462,61 +464,121 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
   }
 }
 
-// Joins the pieces of the item that starts in CTA (or pair) blockIdx.x and goes on
-// after it, in order; one warp a query row.
+// Joins the pieces of the items that are cut: S warps a query row (8 where the grid
+// is large enough for all, down to one), each with every S-th piece, then the warps
+// in order.  The grid fits the GPU at once, so a call without a cut item costs little
+// beyond the launch.
 template <class E, int D, int M>
 __global__ void __launch_bounds__(256) paged_prefill_join_kernel(const __grid_constant__ Args x) {
   constexpr int W = D / 32;                         // dims of a lane: 2, 4 or 8
+  constexpr int PER = MAX_EVEN / 8;                 // items that a warp looks at
   using X = Elem<E>;
+  __shared__ float2 part[8][W / 2][32];
+  __shared__ float2 ml[8];
+  __shared__ int cut[MAX_EVEN], n_cut[8];
   const PagedAttnArgs& a = x.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_items = (int)(x.n_slots * a.hk);
   pdl_wait();
   const Scratch sc = scratch_of(a.scratch);
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const JoinRec rec = sc.rec[c];
-  if (rec.last < 0) return;
-  const Item<M> it(x, rec.w);
-  const int n = rec.last - c + 1;
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (r >= it.rows) return;
-  auto row_of = [&](int i) { return (int64_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * M + r; };
-  float m = -FLT_MAX, l = 0.f, acc[W];
+  // the cut items, in order
+  uint32_t bits[PER / 32];
 #pragma unroll
-  for (int e = 0; e < W; ++e) acc[e] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {              // lane i: the weight of piece i0 + i
-    const float z = i0 + lane < n ? sc.lse2[row_of(i0 + lane)] : -INFINITY;
-    float nm = fmaxf(m, z);
+  for (int i = 0; i < PER / 32; ++i) {
+    const int w = PER * warp + 32 * i + lane;
+    bits[i] = __ballot_sync(0xffffffffu, w < n_items && sc.rec[min(w, MAX_EVEN - 1)].last >= 0);
+  }
+  int mine = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
-    const float f = exp2_approx(m - nm), wz = z == -INFINITY ? 0.f : exp2_approx(z - nm);
-    m = nm;
-    l *= f;
+  for (int i = 0; i < PER / 32; ++i) mine += __popc(bits[i]);
+  if (lane == 0) n_cut[warp] = mine;
+  __syncthreads();
+  int at = 0, all = 0;
 #pragma unroll
-    for (int e = 0; e < W; ++e) acc[e] *= f;
-    const int k = min(32, n - i0);
+  for (int i = 0; i < 8; ++i) {
+    if (i < warp) at += n_cut[i];
+    all += n_cut[i];
+  }
+#pragma unroll
+  for (int i = 0; i < PER / 32; ++i) {
+    if (bits[i] >> lane & 1) cut[at + __popc(bits[i] & ((1u << lane) - 1u))] = PER * warp + 32 * i + lane;
+    at += __popc(bits[i]);
+  }
+  __syncthreads();
+  int S = 8;
+  while (S > 1 && all * (M / 8) * S > (int)gridDim.x) S >>= 1;
+  const int blocks = M / 8 * S;                     // of an item
+  for (int u = blockIdx.x; u < all * blocks; u += gridDim.x) {
+    const int w = cut[u / blocks], sub = warp % S;
+    const JoinRec rec = sc.rec[w];
+    const Item<M> it(x, w);
+    const int r = u % blocks * (8 / S) + warp / S;
+    // pieces of this warp: sub, sub + S, ..
+    const int n = r < it.rows ? (rec.last - rec.first + S - sub) / S : 0;
+    auto row_of = [&](int i) {
+      const int p = i * S + sub;
+      return (int64_t)(2 * (rec.first + p) + (p == 0 ? 1 : 0)) * M + r;
+    };
+    float m = -FLT_MAX, l = 0.f, acc[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) acc[e] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {              // lane i: the weight of piece i0 + i
+      const float z = i0 + lane < n ? sc.lse2[row_of(i0 + lane)] : -INFINITY;
+      float nm = fmaxf(m, z);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
+      const float f = exp2_approx(m - nm), wz = z == -INFINITY ? 0.f : exp2_approx(z - nm);
+      m = nm;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < W; ++e) acc[e] *= f;
+      const int k = min(32, n - i0);
 #pragma unroll 8
-    for (int i = 0; i < k; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, wz, i);
-      const float2* src = reinterpret_cast<const float2*>(sc.o + row_of(i0 + i) * D) + lane;
-      l += wi;
+      for (int i = 0; i < k; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, wz, i);
+        const float2* src = reinterpret_cast<const float2*>(sc.o + row_of(i0 + i) * D) + lane;
+        l += wi;
 #pragma unroll
-      for (int e = 0; e < W / 2; ++e) {               // dims 64 e + 2 lane, + 1
-        const float2 v = src[32 * e];
-        acc[2 * e] = fmaf(wi, v.x, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(wi, v.y, acc[2 * e + 1]);
+        for (int e = 0; e < W / 2; ++e) {               // dims 64 e + 2 lane, + 1
+          const float2 v = src[32 * e];
+          acc[2 * e] = fmaf(wi, v.x, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(wi, v.y, acc[2 * e + 1]);
+        }
       }
     }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int per = a.hq / a.hk;
-  const int64_t flat = it.row0 + r, orow = (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D) + lane;
+    if (S > 1) {
+      __syncthreads();                                // the unit before has been read
+      if (sub > 0) {
 #pragma unroll
-  for (int e = 0; e < W / 2; ++e) dst[32 * e] = X::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        for (int e = 0; e < W / 2; ++e) part[warp][e][lane] = make_float2(acc[2 * e], acc[2 * e + 1]);
+        if (lane == 0) ml[warp] = make_float2(m, l);
+      }
+      __syncthreads();
+      for (int o = warp + 1; sub == 0 && o < warp + S; ++o) {
+        const float2 z = ml[o];
+        const float nm = fmaxf(m, z.x), f = exp2_approx(m - nm), fo = exp2_approx(z.x - nm);
+        m = nm;
+        l = fmaf(l, f, z.y * fo);
+#pragma unroll
+        for (int e = 0; e < W / 2; ++e) {
+          const float2 v = part[o][e][lane];
+          acc[2 * e] = fmaf(acc[2 * e], f, v.x * fo);
+          acc[2 * e + 1] = fmaf(acc[2 * e + 1], f, v.y * fo);
+        }
+      }
+    }
+    if (sub > 0 || r >= it.rows) continue;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t orow = it.q_row(a, (uint32_t)a.hq / (uint32_t)a.hk, it.row0 + r);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D) + lane;
+#pragma unroll
+    for (int e = 0; e < W / 2; ++e) dst[32 * e] = X::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  }
 }
 
 // Whether pairs of CTAs take the batch (paged_prefill_pair.cu): head dim 256,
-// pages that TMA can fetch, and sequences that fill tiles of 256 rows on average.
+// pages that TMA can fetch, and sequences of more rows than a CTA's tile on average.
 bool use_pair(const PagedAttnArgs& a, int head_dim) {
   return head_dim == 256 && paged_prefill_box(a.kv.page_size) > 1 && a.T * (a.hq / a.hk) >= PAIR_ROWS * a.B;
 }
@@ -530,13 +592,15 @@ int walkers_of(const PagedAttnArgs& a, int head_dim, int num_sms) {
   const int most = num_sms < MAX_CTAS ? num_sms : MAX_CTAS;
   return use_pair(a, head_dim) ? most / 2 : most;
 }
-// Whether items may be cut over the CTAs: with no more than two to a CTA one long
-// sequence among them would keep a CTA busy long after the others (64 x 5 tokens
-// over 2000 to 30000 keys: 631 us whole, 250 cut).  With more, or where whole items
-// are quicker after all, it costs 4 to 7 us to find out.
+// Whether items may be cut over the CTAs: where one long sequence would keep a CTA
+// busy long after the others (64 x 5 tokens over 2000 to 30000 keys: 609 us whole,
+// 237 cut; 64 x 21: 574 and 340).  The kernel decides by the lengths; where whole items
+// are quicker after all, it costs 3 to 8 us to find out (64 tokens over 300 keys:
+// 14.4 us and 18; 16 x 100 over 1000: 66 and 74), so batches of more items than a
+// CTA has threads, which are long enough to come out even, are dealt out whole.
 bool may_cut(const PagedAttnArgs& a, int head_dim, int num_sms) {
   const int64_t items = slots_of(a, head_dim) * a.hk;
-  return paged_prefill_box(a.kv.page_size) > 1 && items <= MAX_EVEN && items <= 2 * walkers_of(a, head_dim, num_sms);
+  return paged_prefill_box(a.kv.page_size) > 1 && items <= MAX_EVEN;
 }
 
 template <class E, int D, bool TMA, bool EVEN>
@@ -557,9 +621,9 @@ cudaError_t launch_attn(const Args& x, int grid, cudaStream_t s) {
 }
 
 template <class E, int D, int M>
-cudaError_t launch_join(const Args& x, int walkers, cudaStream_t s) {
+cudaError_t launch_join(const Args& x, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)walkers, M / 8);
+  cfg.gridDim = dim3(JOIN_CTAS);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -581,8 +645,8 @@ cudaError_t launch_d(const PagedAttnArgs& a, const CUtensorMap& tk, int num_sms,
   x.box = paged_prefill_box(a.kv.page_size);
   if (join) {
     if constexpr (D == 256)
-      if (use_pair(a, D)) return launch_join<E, D, 256>(x, walkers, s);
-    return launch_join<E, D, 128>(x, walkers, s);
+      if (use_pair(a, D)) return launch_join<E, D, 256>(x, s);
+    return launch_join<E, D, 128>(x, s);
   }
   if (may_cut(a, D, num_sms)) return launch_attn<E, D, true, true>(x, walkers, s);
   return x.box > 1 ? launch_attn<E, D, true, false>(x, walkers, s) : launch_attn<E, D, false, false>(x, walkers, s);

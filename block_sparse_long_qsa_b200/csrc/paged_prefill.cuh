@@ -33,12 +33,15 @@ struct Tmem {
 };
 constexpr int MAX_CTAS = 160;                       // bound of the scratch (148 SMs on B200)
 constexpr int MAX_EVEN = THREADS;                   // most items that may be cut over the CTAs
-// In tiles (of about 1.8 us): what an item costs beside its own (its queries, the
+// In tiles (of 1 to 2 us): what an item costs beside its own (its queries, the
 // first scores, the last products and the results); the least that is worth a CTA;
-// what the pieces and their join cost.  (37 tokens over 20K keys: whole items 163
-// tiles in a row, cut 15 and 50 us; 16 x 30 tokens over 1000 keys: whole 14 and 29
-// us, cut 10 and 50 us.)
-constexpr int ITEM_COST = 6, LEAST = 4, JOIN_COST = 15;
+// what the pieces and their join cost, with half of the walk for its second and
+// third piece.  (37 tokens over 20K keys: whole 163 tiles in a row and 225 us, cut 8
+// and 40 us; 5 over 1000: 14 and 23.5, 4 and 20.6 us; but 64 over 300: 9 and 18, 4
+// and 21 us; 16 x 100 over 1000: 45 and 79, 32 and 81 us; 2000 over none: 48 and 72,
+// 36 and 79 us.)
+constexpr int ITEM_COST = 6, LEAST = 4, JOIN_COST = 7;
+__host__ __device__ constexpr int64_t cut_cost(int64_t base) { return base + base / 2 + JOIN_COST; }
 // setmaxnreg.inc takes from what the launch allotted: the kernel must have been
 // compiled to the registers that the split adds up to, or it would wait for ever.
 template <class F>
@@ -208,19 +211,19 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// What CTA (or pair) c leaves for the join: the item that starts in its range and
-// goes on in the next ones'.
-struct JoinRec { int64_t w; int32_t last; };
+// What the join needs to know of an item: the CTAs (or pairs) that have its first
+// and its last tile; last -1: one has it whole.
+struct JoinRec { int32_t first, last; };
 // A CTA has up to two pieces of shared items: 2c + 1 of one that starts with it, 2c
 // of one that came in from before; 128 rows of D (a pair's 256) and their base-2
 // log-sum-exp.
 struct Scratch {
-  JoinRec* rec;             // [MAX_CTAS]
+  JoinRec* rec;             // [MAX_EVEN]
   float* lse2;              // [2 MAX_CTAS][128]
   float* o;                 // [2 MAX_CTAS][128][D]
 };
 constexpr size_t REC_BYTES = 4096;
-static_assert(MAX_CTAS * sizeof(JoinRec) <= REC_BYTES, "join records");
+static_assert(MAX_EVEN * sizeof(JoinRec) <= REC_BYTES, "join records");
 __host__ __device__ inline Scratch scratch_of(void* p) {
   uint8_t* u = static_cast<uint8_t*>(p);
   float* f = reinterpret_cast<float*>(u + REC_BYTES);
@@ -236,7 +239,8 @@ struct Args {
 
 // Item w of M query rows.  Sequence b owns the tile slots from cu[b] per / M + b on (at least
 // as many as it has tiles), so a slot's sequence is found by bisection and the
-// slots without a tile are items without keys.
+// slots without a tile are items without keys.  Rows (token, head) of the batch are
+// below 2^30.
 template <int M>
 struct Item {
   int b, g, rows;           // sequence, KV head, rows in use
@@ -244,27 +248,31 @@ struct Item {
   int lo, ns, n_vis;        // key number v: v < ns ? v : lo + v - ns (whole boxes)
   int first, end;           // keys needed: [first, end) and those below the sinks
   int p0;                   // position of the first row's token
-  int64_t t0, row0;         // the sequence's first token row; first flat row of the item
+  int t0, row0;             // the sequence's first token row; first flat row of the item
   __device__ __forceinline__ Item(const Args& x, int64_t w) {
     const PagedAttnArgs& a = x.a;
-    const int per = a.hq / a.hk;
+    const uint32_t per = (uint32_t)a.hq / (uint32_t)a.hk;
     all = n_tiles = tile0 = 0;
-    g = (int)(w % a.hk);
-    const int64_t slot = x.n_slots - 1 - w / a.hk;
+    const int64_t turn = div64(w, a.hk);
+    g = (int)(w - turn * a.hk);
+    const int slot = (int)(x.n_slots - 1 - turn), T = (int)a.T;
+    auto first_slot = [&](int seq, int row) { return (int)((uint32_t)min(max(row, 0), T) * per / M) + seq; };
     int l = 0, h = a.B;
     while (h - l > 1) {
       const int mid = (l + h) >> 1;
-      if ((int64_t)__ldg(a.cu_new + mid) * per / M + mid <= slot) l = mid; else h = mid;
+      if (first_slot(mid, __ldg(a.cu_new + mid)) <= slot) l = mid; else h = mid;
     }
     b = l;
     t0 = __ldg(a.cu_new + b);
-    const int64_t t1 = min((int64_t)__ldg(a.cu_new + b + 1), a.T);
+    const int t1 = min(__ldg(a.cu_new + b + 1), T);
     const int L = __ldg(a.cache_len + b);
-    const int64_t tile = slot - (t0 * per / M + b), n_rows = (t1 - t0) * per;
+    const int tile = slot - first_slot(b, t0);
+    if (t0 < 0 || t0 >= t1 || tile < 0 || L < 0) return;
+    const int n_rows = (t1 - t0) * (int)per;
     row0 = tile * M;
-    rows = (int)min((int64_t)M, n_rows - row0);
-    if (t0 < 0 || tile < 0 || rows <= 0 || L < 0) return;
-    const int64_t pos = L + row0 / per, last = L + (row0 + rows - 1) / per;
+    rows = min(M, n_rows - row0);
+    if (rows <= 0) return;
+    const int64_t pos = (int64_t)L + (uint32_t)row0 / per, last = (int64_t)L + (uint32_t)(row0 + rows - 1) / per;
     end = (int)min(last + 1, (int64_t)a.kv.capacity);
     if (last >= a.kv.capacity) report_error(a.err, QSA_ERR_DEVICE_BOUNDS);
     first = a.window > 0 && pos >= a.window ? (int)min(pos - a.window + 1, (int64_t)end) : 0;
@@ -276,6 +284,11 @@ struct Item {
     // at least one tile: rows whose keys all lie past the table come out zero
     n_tiles = all = max((n_vis + KT - 1) / KT, 1);
   }
+  // Row of q and out of flat row f of the sequence.
+  __device__ __forceinline__ int64_t q_row(const PagedAttnArgs& a, uint32_t per, uint32_t f) const {
+    const uint32_t t = f / per;
+    return (int64_t)(t0 + (int)t) * a.hq + (g * (int)per + (int)(f - t * per));
+  }
   // only tiles [from, to)
   __device__ __forceinline__ void cut(int from, int to) {
     tile0 = from;
@@ -286,11 +299,13 @@ struct Item {
 // The items of a CTA (or pair): w, w + step, .. last; of the first the tiles from
 // `from` on, of the last those before `to`.
 struct Walk {
-  int64_t w, last, step;
+  int w, last, step;
   int from, to;
 };
+// Number of an item: of up to MAX_EVEN that may be cut, or of any.
+template <bool EVEN> using ItemNo = std::conditional_t<EVEN, int, int64_t>;
 template <int M, bool EVEN>
-__device__ __forceinline__ Item<M> item_of(const Args& x, const Walk& k, int64_t w) {
+__device__ __forceinline__ Item<M> item_of(const Args& x, const Walk& k, ItemNo<EVEN> w) {
   Item<M> it(x, w);
   if (EVEN && it.n_tiles > 0) it.cut(w == k.w ? k.from : 0, w == k.last ? k.to : INT32_MAX);
   return it;
@@ -302,46 +317,59 @@ __device__ __forceinline__ Walk uniform(const Walk& k) {
 }
 // All threads of a CTA, once: the walk of CTA (or pair) c of n over up to MAX_EVEN
 // items.  ITEM_COST units and a unit a tile for each, end to end, cut evenly, where
-// that is quicker than whole items in turn.  Each thread counts one item's; those
-// that hold the range's ends write them down.  buf: 2.5 KB of shared memory.
+// that is quicker than whole items in turn (of those with tiles, if they are no more
+// than two to a CTA, else of all).  Each thread counts one item's; those that hold
+// the range's ends write them down.  buf: 3 KB of shared memory.
 template <int M>
 __device__ __forceinline__ Walk make_walk(const Args& x, int c, int n, void* buf) {
-  const int64_t n_items = x.n_slots * x.a.hk;
+  const int n_items = (int)(x.n_slots * x.a.hk);
   int64_t* sum = static_cast<int64_t*>(buf);                        // [16]
   Walk* out = reinterpret_cast<Walk*>(sum + 16);
-  int32_t* item = reinterpret_cast<int32_t*>(out + 1);              // [MAX_EVEN]
+  int32_t* item = reinterpret_cast<int32_t*>(out + 1);              // [MAX_EVEN] the items with tiles
+  int32_t* whole = item + MAX_EVEN;                                 // [MAX_CTAS] units of a CTA that takes whole items
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Scratch sc = scratch_of(x.a.scratch);
   const int tiles = tid < n_items ? Item<M>(x, tid).all : 0;
   const int64_t units = tiles ? tiles + ITEM_COST : 0;
-  int64_t s = units;
+  constexpr int64_t ONE = (int64_t)1 << 40;                         // sums: units, and above them items
+  const int64_t mine = tiles ? ONE + units : 0;
+  int64_t s = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += v;
   }
   if (lane == 31) sum[warp] = s;
-  item[tid] = (int32_t)units;
-  if (tid == 0) {
-    *out = {0, -1, 1, 0, 0};
-    sc.rec[c] = {0, -1};
-  }
+  if (tid < MAX_CTAS) whole[tid] = 0;
+  if (tid == 0) *out = {0, -1, 1, 0, 0};
   __syncthreads();
-  // the longest walk of whole items
-  int64_t whole = 0;
-  if (tid < n)
-    for (int64_t i = tid; i < n_items; i += n) whole += item[i];
-  int64_t total = 0, at = s - units;                                // at: units before this item's
+  int64_t total = 0, at = s - mine;                                 // at: before this item
 #pragma unroll
   for (int i = 0; i < THREADS / 32; ++i) {
     if (i < warp) at += sum[i];
     total += sum[i];
   }
+  const int busy = (int)(total / ONE), rank = (int)(at / ONE);      // items with tiles; those before this one
+  const bool two = busy <= 2 * n;
+  total %= ONE;
+  at %= ONE;
+  if (tiles) {
+    item[rank] = tid;
+    atomicAdd(&whole[(two ? rank : tid) % n], (int)units);
+  }
+  __syncthreads();
   // CTA c has the units from c base + min(c, more) on: base, or one more; CTAs
   // beyond what is worth one have none
   const int64_t parts = min((int64_t)n, max(total / LEAST, (int64_t)1));
-  const int64_t base = total / parts, more = total - base * parts;
-  if (!__syncthreads_or(whole > base + JOIN_COST)) return {c, n_items - 1, n, 0, INT32_MAX};
+  const int64_t base = div64(total, parts), more = total - base * parts;
+  const bool cut = __syncthreads_or(tid < n && whole[tid] > cut_cost(base));
+  if (c == 0 && tid < n_items && (!cut || !units)) sc.rec[tid] = {0, -1};
+  if (!cut && !two) return {c, n_items - 1, n, 0, INT32_MAX};
+  if (!cut) {
+    if (c >= busy) return {0, -1, 1, 0, 0};
+    const int w = item[c], last = c + n < busy ? item[c + n] : w;
+    return {w, last, max(last - w, 1), 0, INT32_MAX};
+  }
   if (c < parts && units) {
     const int64_t ua = c * base + min((int64_t)c, more), ub = ua + base + (c < more ? 1 : 0);
     const int64_t tile0 = at + ITEM_COST, end = tile0 + tiles;      // the item's tiles
@@ -354,9 +382,10 @@ __device__ __forceinline__ Walk make_walk(const Args& x, int c, int n, void* buf
       out->last = tid;
       out->to = to;
     }
-    if (ua < end && ub > tile0 && from == 0 && to < tiles) {        // its first tile is here, its last is not
+    if (ua <= tile0 && tile0 < ub) {                                // its first tile is here
       const int64_t u = end - 1;
-      sc.rec[c] = {tid, (int32_t)(u < more * (base + 1) ? u / (base + 1) : more + (u - more * (base + 1)) / base)};
+      const int64_t last = u < more * (base + 1) ? div64(u, base + 1) : more + div64(u - more * (base + 1), base);
+      sc.rec[tid] = {c, to < tiles ? (int32_t)last : -1};
     }
   }
   __syncthreads();
@@ -371,13 +400,13 @@ struct SoftBars {
 };
 template <class E, int D, int ROWS, bool PAIR, bool EVEN>
 __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint32_t off_ok, uint32_t off_xch, const SoftBars& bar,
-                                             uint32_t tmem, int warp, int lane, int r0, const Walk& walk, int64_t w_first, int64_t w_last,
-                                             int64_t w_step, int cta,
+                                             uint32_t tmem, int warp, int lane, int r0, const Walk& walk, ItemNo<EVEN> w_first,
+                                             ItemNo<EVEN> w_last, ItemNo<EVEN> w_step, int cta,
                                              volatile int* abort_flag) {
   using X = Elem<E>;
   using TM = Tmem<D, PAIR>;
   const PagedAttnArgs& a = x.a;
-  const int per = a.hq / a.hk;
+  const uint32_t per = (uint32_t)a.hq / (uint32_t)a.hk;
   const int quad = warp & 3, wg = warp >> 2;      // rows 32 quad .., tiles with count % 2 == wg
   const int r = 32 * quad + lane;
   const uint32_t lanes = (uint32_t)(32 * quad) << 16;
@@ -388,7 +417,7 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, bar_wait<PAIR>(bar, parity, abort_flag, a.err));
   };
-  for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+  for (ItemNo<EVEN> w = w_first; ok && w <= w_last; w += w_step) {
     int n_tiles, v0;                                // tiles of the item, first key number of the tile
     int v_min, v_max;                               // the row sees v in [v_min, v_max] and v < sinks
     int all_min, all_max;                           // every row sees v in [all_min, all_max]
@@ -400,17 +429,17 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
       n_tiles = it.n_tiles;
       v0 = it.tile0 * KT;
       const bool in = r0 + r < it.rows;
-      const int64_t flat = it.row0 + (in ? r0 + r : 0), tok0 = it.row0 / per;
+      const uint32_t flat = it.row0 + (in ? r0 + r : 0), row0 = it.row0, tok0 = row0 / per;
       const int shift = it.ns - it.lo;              // position -> number, behind the gap
-      const int64_t pos = (int64_t)it.p0 + (flat / per - tok0);
-      const int64_t pos1 = (int64_t)it.p0 + ((it.row0 + min(it.rows, r0 + 128) - 1) / per - tok0);
-      const int64_t pos_f = (int64_t)it.p0 + ((it.row0 + min(r0, it.rows - 1)) / per - tok0);
+      const int64_t pos = (int64_t)it.p0 + (int)(flat / per - tok0);
+      const int64_t pos1 = (int64_t)it.p0 + (int)((row0 + min(it.rows, r0 + 128) - 1) / per - tok0);
+      const int64_t pos_f = (int64_t)it.p0 + (int)((row0 + min(r0, it.rows - 1)) / per - tok0);
       v_max = (int)min(pos + shift, (int64_t)it.n_vis - 1);
       all_max = (int)min(pos_f + shift, (int64_t)it.n_vis - 1);
       v_min = a.window > 0 ? (int)max(pos - a.window + 1 + shift, (int64_t)0) : 0;
       all_min = a.window > 0 ? (int)max(pos1 - a.window + 1 + shift, (int64_t)0) : 0;
       part = EVEN && it.n_tiles < it.all;
-      orow = !in ? -1 : part ? (int64_t)(2 * cta + (it.tile0 == 0 ? 1 : 0)) * ROWS + r0 + r : (it.t0 + flat / per) * a.hq + it.g * per + flat % per;
+      orow = !in ? -1 : part ? (int64_t)(2 * cta + (it.tile0 == 0 ? 1 : 0)) * ROWS + r0 + r : it.q_row(a, per, flat);
     }
     float m = -FLT_MAX, l = 0.f;
     for (int i = (int)((count ^ wg) & 1); i < n_tiles; i += 2) {

@@ -1,5 +1,5 @@
 // Attention of a ragged batch of new tokens over their pages (qsa_paged_prefill)
-// for head dim 256 and batches of long sequences: one MMA over two CTAs.
+// for head dim 256 and sequences of more than 128 query rows: one MMA over two CTAs.
 //
 // The mathematics, the numbering of the keys and the softmax are those of
 // paged_prefill.cu.  There one CTA's tile of 128 rows needs 128 KB of K and V per
@@ -21,7 +21,7 @@
 // milliseconds, by the power limit: 32768 tokens of 24 + 2 heads of 256 take 9.4
 // to 10.2 ms, 1290 to 1410 TFLOP/s by the clock that is left; 16384 tokens 2.4 ms
 // with the tensor pipe 70 % busy; 8 sequences of up to 8192 with a window of 1024
-// keys 0.67 ms, 830 TFLOP/s of visible pairs (the tiles at both ends of a window are
+// keys 0.58 ms, 960 TFLOP/s of visible pairs (the tiles at both ends of a window are
 // half masked).
 #include "paged_prefill.cuh"
 
@@ -101,13 +101,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
   // the roles' loops would have to read)
   Walk walk{};
   if constexpr (EVEN) walk = uniform(make_walk<M>(x, blockIdx.x >> 1, gridDim.x >> 1, smem));   // in Q's place
-  const int64_t w_first = EVEN ? walk.w : (int64_t)(blockIdx.x >> 1), w_step = EVEN ? walk.step : (int64_t)(gridDim.x >> 1);
-  const int64_t w_last = EVEN ? walk.last : x.n_slots * x.a.hk - 1;
+  const ItemNo<EVEN> w_first = EVEN ? walk.w : (blockIdx.x >> 1), w_step = EVEN ? walk.step : (gridDim.x >> 1);
+  const ItemNo<EVEN> w_last = EVEN ? walk.last : x.n_slots * x.a.hk - 1;
   __syncthreads();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int per = a.hq / a.hk;
+  const uint32_t per = (uint32_t)a.hq / (uint32_t)a.hk;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag, a.err));
   };
@@ -120,7 +120,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
     // ---------------------------------------------------------------------- Q
     const int lt = tid - 32 * W_LOAD, c = lt & 7, rt = lt >> 3;
     uint32_t items_done = 0;
-    for (int64_t w = w_first; w <= w_last; w += w_step) {
+    for (ItemNo<EVEN> w = w_first; w <= w_last; w += w_step) {
       const Item<M> it = item_of<M, EVEN>(x, walk, w);
       if (it.n_tiles <= 0) continue;
       // once the previous item's last S has read its own
@@ -129,8 +129,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
       for (int j = 0; j < RJ; ++j) {
         const int r = 128 * rank + RT * j + rt;
         const bool valid = r < it.rows;
-        const int64_t f = it.row0 + (valid ? r : 0);
-        const uint16_t* src = a.q + ((it.t0 + f / per) * a.hq + it.g * per + f % per) * D + 8 * c;
+        const uint32_t f = it.row0 + (valid ? r : 0);
+        const uint16_t* src = a.q + it.q_row(a, per, f) * D + 8 * c;
 #pragma unroll
         for (int ch = 0; ch < D / 64; ++ch)
           cp_async16_zfill(smem_u32(smem + ch * 16384) + swz128(RT * j + rt, c), src + 64 * ch, valid);
@@ -147,7 +147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
     uint32_t kph = 1, vph = 1, count = 0, k_used = 0, v_used = 0;   // used: stages that copies went to
     bool ok = true;
     const int box = x.box, nb = KT / box, nbk = nb / 2;            // boxes of a tile; of a K half
-    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+    for (ItemNo<EVEN> w = w_first; ok && w <= w_last; w += w_step) {
       const Item<M> it = item_of<M, EVEN>(x, walk, w);
       if (it.n_tiles <= 0) continue;
       const int32_t* table = a.kv.table + (int64_t)it.b * a.kv.table_ld;
@@ -227,7 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
     uint32_t kph = 0, items_done = 0, count = 0;
     bool ok = true;
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
-    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+    for (ItemNo<EVEN> w = w_first; ok && w <= w_last; w += w_step) {
       const Item<M> it = item_of<M, EVEN>(x, walk, w);
       const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
       if (n_tiles <= 0) continue;
@@ -277,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
     uint32_t vph = 0, items_done = 0, count = 0;
     bool ok = true;
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
-    for (int64_t w = w_first; ok && w <= w_last; w += w_step) {
+    for (ItemNo<EVEN> w = w_first; ok && w <= w_last; w += w_step) {
       const Item<M> it = item_of<M, EVEN>(x, walk, w);
       const int n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
       if (n_tiles <= 0) continue;
