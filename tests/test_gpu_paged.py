@@ -539,7 +539,13 @@ def test_prefill_of_one_token_each_is_a_decode():
     ((28, 4, 128), [4000, 0], [30, 300]),
     ((16, 16, 64), [100], [1300]),
     ((16, 16, 64), [8000], [3]),
-    ((64, 1, 128), [33], [700])])
+    ((64, 1, 128), [33], [700]),
+    ((24, 2, 256), [9000], [11]),                       # a pair with few rows in its second half, many pieces
+    ((24, 2, 256), [100] * 47 + [12000], [21] * 48),    # pairs, more items than pairs, one of them long
+    ((24, 2, 256), [50] * 100 + [15000, -1], [2] * 102),    # single CTAs, likewise, a padding sequence
+    ((32, 8, 128), [0, 40] * 20 + [9000], [3] * 41),    # 656 items: no cut
+    ((32, 8, 128), [0, 40] * 10 + [9000], [3, 1] * 10 + [1]),
+    ((24, 2, 256), [0] * 30, [3, 70, 120] * 10)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (700, 5)])
 def test_prefill_ways_to_deal_the_tiles(heads, cached, new, window, sinks):
     """Each kernel and each way to deal the tiles to the CTAs, twice with the same bits."""
