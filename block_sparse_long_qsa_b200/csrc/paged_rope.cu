@@ -40,10 +40,10 @@ __global__ void __launch_bounds__(32 * WARPS) norm_rope_kernel(const __grid_cons
   __shared__ float2 cs_all[WARPS][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % G, sub = lane / G;
-  const int64_t unit = (int64_t)blockIdx.x * WARPS + warp;
-  const int64_t t = unit / a.parts;
+  const uint32_t unit = blockIdx.x * WARPS + warp;   // T parts < 2^31
+  const int64_t t = unit / (uint32_t)a.parts;
   if (t >= a.T) return;
-  const int part = (int)(unit - t * a.parts);
+  const int part = (int)(unit - (uint32_t)t * (uint32_t)a.parts);
   float2* cs = cs_all[warp];
   const int n_q = a.q ? a.hq : 0, n_k = a.k ? a.hk : 0, n_v = APPEND ? a.hk : 0;
 
