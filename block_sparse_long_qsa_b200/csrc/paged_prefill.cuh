@@ -54,8 +54,8 @@ cudaError_t prepare_launch(F* kernel, uint32_t smem) {
 }
 // Quarter of a tile's exponentials after which the next tile's begin (32K tokens
 // of 24 + 2 heads of 256: 9.65 ms with 1, 9.85 with 2, 9.87 without turns; 16K of
-// 16 heads of 64: 1.20 ms with 1, 1.19 with 2, 1.27 without; 128: 3.0 ms with 1,
-// 2.6 with 2 and without).
+// 16 heads of 64: 0.95 ms with 1, 0.84 to 0.91 with 2, 0.85 with 3; 12000 of 32 + 8
+// heads of 128: 1.07 ms with 1, 1.09 with 2, 1.10 with 3).
 __host__ __device__ constexpr int turn_after(int D) { return D == 256 ? 1 : 2; }
 constexpr float RAISE = 8.f;                        // lazy maximum: P stays below 2^8
 
