@@ -112,8 +112,9 @@ __global__ void __launch_bounds__(32 * WARPS) norm_rope_kernel(const __grid_cons
   const bool rot = l < 2 * hl;
   const int partner = l < hl ? l + hl : (rot ? l - hl : l);
 
-  // rows [r0, r1) of q or of k; x holds the first step's when loaded
-  auto turn = [&](const uint16_t* row, int r0, int r1, const uint16_t* weight, uint16_t* out, bool loaded) {
+  // rows [r0, r1) of q or of k to out, out_ld elements apart; x holds the first
+  // step's when loaded.  (q and k may be one tensor: nothing goes by their addresses.)
+  auto turn = [&](const uint16_t* row, int r0, int r1, const uint16_t* weight, uint16_t* out, int64_t out_ld, bool loaded) {
     if (r0 >= r1) return;
     uint64_t cw[4], sw[4];
     {
@@ -182,15 +183,14 @@ __global__ void __launch_bounds__(32 * WARPS) norm_rope_kernel(const __grid_cons
           w[e] = X::pack(y0, y1);
         }
         if (out && r + u * RPW + sub < r1)
-          *reinterpret_cast<uint4*>(out + (int64_t)(r + u * RPW + sub) * (APPEND && row == k_row ? a.kv.head_stride : D)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(out + (int64_t)(r + u * RPW + sub) * out_ld) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   };
   const bool has_q = q0 < q1, has_k = k0 < k1;
-  turn(q_row, q0, q1, a.q_weight, a.q_out + t * a.hq * D + 8 * l, true);
+  turn(q_row, q0, q1, a.q_weight, a.q_out + t * a.hq * D + 8 * l, D, true);
   uint16_t* k_out = APPEND ? (page_off >= 0 ? a.kv.k + page_off + 8 * l : nullptr) : a.k_out + t * a.hk * D + 8 * l;
-  turn(k_row, k0, k1, a.k_weight, k_out, !has_q);
+  turn(k_row, k0, k1, a.k_weight, k_out, APPEND ? a.kv.head_stride : D, !has_q);
   if (APPEND && page_off >= 0) {
     bool loaded = !has_q && !has_k;
     for (int r = v0; r < v1; r += STEP) {

@@ -162,6 +162,30 @@ def test_append(heads, dt, page, layout):
     assert bool(cache.k[~written].isnan().all()) and bool(cache.v[~written].isnan().all())
 
 
+@pytest.mark.parametrize("layout", ["head", "beside"])
+@pytest.mark.parametrize("T", [5, 3100])
+@pytest.mark.parametrize("same", ["tensor", "start"])
+def test_append_where_queries_and_keys_are_one_tensor(same, T, layout):
+    """A shared projection (as many query as KV heads, or fewer KV heads from the
+    same first element) with a weight each, into caches whose heads do not lie
+    side by side; nothing behind q_out is written."""
+    hq, hk, D, page = (4, 4, 128, 16) if same == "tensor" else (6, 2, 128, 16)
+    p = qsa.layer_params(hq, hk, D)
+    g = gen(T)
+    cache = U.Cache(p, [7 + T], page, BF, "cuda", layout)
+    x, v, qw, kw = randn(g, BF, T, hq, D), randn(g, BF, T, hk, D), randn(g, BF, D), randn(g, BF, D)
+    qo = torch.full((3 * T, hq, D), 5.0, dtype=BF, device="cuda")
+    cu, cl = (torch.tensor(n, dtype=torch.int32, device="cuda") for n in ([0, T], [7]))
+    ws = qsa.paged_workspace(p, 1, T)
+    qsa.qsa_paged_append(p, cache.kv, 1, T, cu, cl, x[:, :hk], v, ws, q=x, q_out=qo, q_weight=qw, k_weight=kw)
+    assert ok(ws) == 0
+    at = 7 + torch.arange(T, device="cuda")
+    U.check_norm_rope(qo[:T], *U.norm_rope64(p, x, qw, at[None]), BF)
+    pg, sl = cache.slots(0, at)
+    U.check_norm_rope(cache.k[pg, sl], *U.norm_rope64(p, x[:, :hk], kw, at[None]), BF)
+    assert torch.equal(cache.v[pg, sl], v) and bool((qo[T:] == 5).all())
+
+
 def test_append_one_token_each_without_queries():
     hq, hk, D, B = 8, 4, 128, 70
     p = qsa.layer_params(hq, hk, D, rope_axes=3)
