@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_prefill_kernel(const __grid_
         row = row_n;
         const uint32_t good = __ballot_sync(0xffffffffu, id >= 0);
         reinterpret_cast<volatile uint8_t*>(smem + OFF_OK)[(count % NOK) * 32 + lane] = good >> (4 * lane / box) & 1 ? 15 : 0;
+        __syncwarp();                              // every lane's bits before the arrival that lane 0 makes
         ++count;
         if (i + 1 < it.n_tiles) find(it.tile0 + i + 1, id_n, row_n);
         const bool mine = lane < nb && id >= 0;

@@ -172,6 +172,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) paged_pr
         if (i < it.n_tiles) {
           const uint32_t good = __ballot_sync(0xffffffffu, id >= 0);
           reinterpret_cast<volatile uint8_t*>(smem + OFF_OK)[(count % NOK) * 32 + lane] = good >> (4 * lane / box) & 1 ? 15 : 0;
+          __syncwarp();                              // every lane's bits before the arrival that lane 0 makes
           ++count;
           if (i + 1 < it.n_tiles) find(it.tile0 + i + 1, id_n, row_n);
           // K: this CTA's 64 keys; lane: box of the half, chunk of 64 dims

@@ -443,6 +443,42 @@ def test_prefill_window(heads, window, sinks):
     check_batch(p, cache, cached, new, q, out, lse, BF, some)
 
 
+def hide(p, cache, cached, new):
+    """NaN in every slot of the sequences' pages that no token of the call sees."""
+    for b, (c, n) in enumerate(zip(cached, new)):
+        if c < 0 or n == 0:
+            continue
+        seen = torch.zeros(cache.table.shape[1] * cache.page, dtype=torch.bool)
+        for i in range(n):
+            seen[U.visible(p, c + i)] = True
+        pages = (cache.table[b] >= 0).cpu().nonzero().flatten()
+        keys = (pages[:, None] * cache.page + torch.arange(cache.page)).flatten()
+        pg, sl = cache.slots(b, keys[~seen[keys]].cuda())
+        cache.k[pg, sl] = float("nan")
+        cache.v[pg, sl] = float("nan")
+
+
+@pytest.mark.parametrize("heads", [(24, 2, 256), (28, 4, 128), (16, 16, 64)])
+@pytest.mark.parametrize("page,layout", [(16, "token"), (48, "beside"), (64, "head"), (64, "beside"), (24, "token")])
+@pytest.mark.parametrize("window,sinks", [(70, 0), (70, 5), (300, 17), (1000, 100)])
+def test_slots_that_no_token_sees_may_hold_anything(heads, page, layout, window, sinks):
+    """Pages of which the window or the sinks leave a part: the other slots are NaN."""
+    p = qsa.layer_params(*heads, window=window, n_sinks=sinks)
+    for cached, new in (([window + 333, 0, 50, 5003], [200, 131, 70, 30]), ([window + 333, 9, 5003], [3, 2, 1])):
+        cache, q, cl, cu = batch(p, cached, new, page, BF, layout, seed=window)
+        hide(p, cache, cached, new)
+        out, lse, ws = run_prefill(p, cache, q, cl, cu)
+        assert ok(ws) == 0
+        check_batch(p, cache, cached, new, q, out, lse, BF, some)
+        assert bool(out.isfinite().all())
+    one = [1] * len(cached)
+    cache, q, cl, _ = batch(p, cached, one, page, BF, layout, seed=window + 1)
+    hide(p, cache, cached, one)
+    out, lse, ws = run_decode(p, cache, q, cl)
+    assert ok(ws) == 0
+    check_batch(p, cache, cached, one, q, out, lse, BF)
+
+
 @pytest.mark.parametrize("heads", [(24, 2, 256), (28, 4, 128)])
 @pytest.mark.parametrize("window,sinks", [(100, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 0)])
 def test_window_and_sinks_of_any_size(heads, window, sinks):
