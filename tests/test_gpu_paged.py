@@ -479,6 +479,19 @@ def test_slots_that_no_token_sees_may_hold_anything(heads, page, layout, window,
     check_batch(p, cache, cached, one, q, out, lse, BF)
 
 
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("dt,page", [(BF, 16), (FP, 48), (BF, 64)])
+def test_prefill_keys_and_values_side_by_side(heads, dt, page):
+    """Keys and values of a page side by side with a gap behind each row, in page
+    sizes that go through tensor maps."""
+    p = qsa.layer_params(*heads, dtype=dt)
+    for cached, new in (([0, 3, 130, -1, 0, 1000, 127], [1, 200, 5, 7, 0, 40, 131]), ([3000, 20], [9, 2])):
+        cache, q, cl, cu = batch(p, cached, new, page, dt, "beside")
+        out, lse, ws = run_prefill(p, cache, q, cl, cu)
+        assert ok(ws) == 0
+        check_batch(p, cache, cached, new, q, out, lse, dt, some)
+
+
 @pytest.mark.parametrize("heads", [(24, 2, 256), (28, 4, 128)])
 @pytest.mark.parametrize("window,sinks", [(100, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 0)])
 def test_window_and_sinks_of_any_size(heads, window, sinks):
