@@ -27,6 +27,7 @@
 // of 64 on one KV head, of which an item takes 16, so the keys are read three
 // times: 176 us where one reading takes 57.
 #include <cfloat>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -43,6 +44,11 @@ constexpr int RING = 196608;                      // all slots
 constexpr int ROWS = 16;
 constexpr int MAX_CTAS = 160;                     // bound of the scratch (148 SMs on B200)
 constexpr int MAX_B = 4096;
+// The weights are held times 2^shift.  In fp16, whose normal numbers end at 2^-14,
+// a first key that outweighs the others would else leave them few bits, and none
+// below 2^-25 of its weight; the largest, 2^15, still fits.
+template <class E>
+constexpr float P_SHIFT = std::is_same<E, __half>::value ? 15.f : 0.f;
 constexpr uint32_t OFF_Q = RING;                  // 16 rows of queries
 constexpr uint32_t OFF_P = OFF_Q + ROWS * 512;    // running units of the sequences, MAX_B + 1
 constexpr uint32_t OFF_V = OFF_P + 4 * (MAX_B + 4);
@@ -362,8 +368,8 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
             o[n][3] *= c1;
           }
         }
-        const float s0 = m0 == -INFINITY ? 0.f : m0, s1 = m1 == -INFINITY ? 0.f : m1;
-        // p <= 1; the sum takes the fp32 values, the products p rounded to 16 bits
+        const float s0 = (m0 == -INFINITY ? 0.f : m0) - P_SHIFT<E>, s1 = (m1 == -INFINITY ? 0.f : m1) - P_SHIFT<E>;
+        // p <= 2^P_SHIFT; the sum takes the fp32 values, the products p rounded to 16 bits
         // (relative error half an ulp of the type, as for the inputs themselves)
         uint32_t pa[KT / 16][4];
 #pragma unroll
@@ -430,7 +436,7 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
       const float inv = l == 0.f ? 0.f : 1.f / l;  // no key at all: zero
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) ml[w * ROWS + tid].x = f[w] * inv;
-      const float lse2 = l == 0.f ? -INFINITY : mx + log2f(l);
+      const float lse2 = l == 0.f ? -INFINITY : mx + log2f(l) - P_SHIFT<E>;
       if (!whole) sc.lse2[piece * ROWS + tid] = lse2;
       else if (a.lse) a.lse[qrow + tid] = lse2 * 0.69314718055994531f;
     }

@@ -566,6 +566,61 @@ def test_prefill_long_prefix_few_rows():
         assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+def check_weights(q, k, v, scale, got, got_lse, dt, shift):
+    """A row of queries [H][D] over keys and values [n][Hk][D], all visible, whose
+    weights span more than the element type: each weight has an error of half a
+    step, or, below the type's normal numbers, of half the smallest one, 2^-25 in
+    fp16, of weights that the kernels hold 2^shift times as large (relative to the
+    largest, whose sum is at least that); scores, sums and result as in check_row."""
+    H, D = q.shape
+    per = H // k.shape[1]
+    k, v = k.repeat_interleave(per, 1), v.repeat_interleave(per, 1)
+    s = torch.einsum("hd,nhd->hn", q.double(), k) * scale
+    w = (s - s.logsumexp(1, keepdim=True)).exp()
+    delta = 2 * D * 2.0 ** -24 * scale * torch.einsum("hd,nhd->hn", q.double().abs(), k.abs())   # of each score
+    want = torch.einsum("hn,nhd->hd", w, v)
+    shared = (w * delta).sum(1)                                        # of the sum, relative
+    size = torch.einsum("hn,nhd->hd", w * (U.half_step(dt) + 2 * delta + 2 * shared[:, None] + (k.shape[0] + 64) * 2.0 ** -23), v.abs())
+    low = 2.0 ** (-25 - shift) * v.abs().sum(0) + 2.0 ** -25 if dt == FP else 0.0
+    err = (got.double() - want).abs()
+    tol = U.half_step(dt) * want.abs() + size + low
+    assert bool((err <= tol).all()), (float((err / want.abs()).max()), float((err - tol).max()))
+    # log-sum-exp: the sum's relative error, the score of its maximum, log2 and the product
+    lse = s.logsumexp(1)
+    assert bool(((got_lse.double() - lse).abs() <= shared + delta.amax(1) + (k.shape[0] + 64) * 2.0 ** -23 + 2.0 ** -22 * (lse.abs() + 20)).all())
+
+
+@pytest.mark.parametrize("heads", [(24, 2, 256), (28, 4, 128), (16, 16, 64)])
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("gap", [6.0, 13.0, 18.0])
+def test_first_key_that_outweighs_the_others(heads, dt, gap):
+    """A first key whose score lies `gap` above all others and whose value is zero,
+    as models learn them: the result is the others' small weights alone."""
+    hq, hk, D = heads
+    p = qsa.layer_params(*heads, dtype=dt)
+    n, g = 700, gen(int(gap))
+    cache = U.Cache(p, [n] * 3, 16, dt, "cuda")
+    u = torch.sign(torch.randn(D, generator=g)).cuda()
+    for b in range(3):
+        k, v = 0.05 * randn(g, dt, n, hk, D), 1 + 0.2 * randn(g, dt, n, hk, D)
+        k[0], v[0] = (gap / D ** 0.5 * u).to(dt), 0
+        cache.fill(b, 0, n, k, v)
+    new = [9, 200, 1]                           # the last tokens of each sequence
+    q = (u + 0.01 * randn(g, dt, sum(new), hq, D)).to(dt)
+    cl, cu = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([n - m for m in new], [0, 9, 209, 210]))
+    out, lse, ws = run_prefill(p, cache, q, cl, cu)
+    last = torch.tensor([8, 208, 209], device="cuda")
+    end = torch.full((3,), n - 1, dtype=torch.int32, device="cuda")
+    d_out, d_lse, _ = run_decode(p, cache, q[last].contiguous(), end, ws)
+    assert ok(ws) == 0
+    for row, b, m in ((0, 0, n - 8), (8, 0, n), (9, 1, n - 199), (150, 1, n - 58), (208, 1, n), (209, 2, n)):
+        k, v = cache.rows(b, torch.arange(m).cuda())
+        check_weights(q[row], k, v, D ** -0.5, out[row], lse[row], dt, 7)
+    for b in range(3):
+        k, v = cache.rows(b, torch.arange(n).cuda())
+        check_weights(q[last[b]], k, v, D ** -0.5, d_out[b], d_lse[b], dt, 15)
+
+
 @pytest.mark.parametrize("dt", [BF, FP])
 def test_prefill_large_scores(dt):
     p = qsa.layer_params(24, 2, 256, dtype=dt, softmax_scale=1.0)
