@@ -72,17 +72,21 @@ float softmax_scale(const qsa_params* p) {
 // original context, L f_i / (2 pi), equals n is d ln(L / (2 pi n)) /
 // (2 ln theta); pairs before the beta_fast index (rounded down) keep f_i, pairs
 // after the beta_slow index (rounded up) take f_i / s, linear in the index in
-// between.  P is qsa_params or qsa_layer_params.
+// between.  Where both indices lie before the pairs all are divided, where both
+// lie behind them none is.  P is qsa_params or qsa_layer_params.
 template <class P>
 void inv_freq(const P* p, double* f) {
   const int half = p->rope_dim / 2;
   const double d = (double)p->rope_dim, s = p->yarn_factor;
   double lo = 0.0, hi = 1.0;
+  bool none = false, all = false;
   if (s > 1.0) {
     const double two_pi = 6.283185307179586476925286766559;
     const double ln_theta = std::log(p->rope_theta);
     lo = std::floor(d * std::log(p->yarn_original_max / (two_pi * p->yarn_beta_fast)) / (2.0 * ln_theta));
     hi = std::ceil(d * std::log(p->yarn_original_max / (two_pi * p->yarn_beta_slow)) / (2.0 * ln_theta));
+    none = lo >= d - 1.0;
+    all = hi <= 0.0;
     lo = std::max(lo, 0.0);
     hi = std::min(hi, d - 1.0);
     if (hi == lo) hi += 0.001;
@@ -93,7 +97,7 @@ void inv_freq(const P* p, double* f) {
       f[i] = base;
       continue;
     }
-    const double t = std::min(std::max(((double)i - lo) / (hi - lo), 0.0), 1.0);   // share of f / s
+    const double t = none ? 0.0 : all ? 1.0 : std::min(std::max(((double)i - lo) / (hi - lo), 0.0), 1.0);   // share of f / s
     f[i] = base / s * t + base * (1.0 - t);
   }
 }
@@ -1406,3 +1410,13 @@ qsa_status qsa_paged_prefill(const qsa_layer_params* p, const qsa_paged_kv* kv, 
 }
 
 }  // extern "C"
+
+#ifdef QSA_DEBUG_HOOKS
+extern "C" qsa_status qsa_debug_rope_frequencies(const qsa_layer_params* p, double* f) {
+  const qsa_status st = check_layer(p);
+  if (st != QSA_OK) return st;
+  if (!f) return QSA_ERR_INVALID_ARG;
+  inv_freq(p, f);
+  return QSA_OK;
+}
+#endif

@@ -92,7 +92,8 @@ typedef struct {
    * yarn_original_max tokens, gets f_i / s if it fits fewer than
    * yarn_beta_slow (default 1) times, and a linear mix in i in between
    * (ends: the indices where the count crosses the two betas, rounded down /
-   * up); the rotated dims of q and k are multiplied by 0.1 ln s + 1. */
+   * up; where both lie before the first pair or behind the last, all pairs
+   * are divided or none); the rotated dims of q and k are multiplied by 0.1 ln s + 1. */
   double yarn_factor;
   double yarn_original_max;
   double yarn_beta_fast;

@@ -47,6 +47,9 @@ enum {
  * call replaces an armed code).  QSA_ERR_INVALID_ARG for an unknown code. */
 qsa_status qsa_debug_inject(int32_t code);
 
+/* The rope_dim / 2 rotary frequencies of a layer (host array), YaRN included. */
+qsa_status qsa_debug_rope_frequencies(const qsa_layer_params* p, double* f);
+
 #ifdef __cplusplus
 }
 #endif

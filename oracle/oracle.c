@@ -96,6 +96,8 @@ static double rope_freq(const oracle_params* p, int i) {
   const double i_fast = d * log(p->yarn_original_max / (two_pi * p->yarn_beta_fast)) / (2.0 * log(p->rope_theta));
   const double i_slow = d * log(p->yarn_original_max / (two_pi * p->yarn_beta_slow)) / (2.0 * log(p->rope_theta));
   double lo = floor(i_fast), hi = ceil(i_slow);
+  if (hi <= 0.0) return f / s;                  /* both crossings before the pairs */
+  if (lo >= d - 1.0) return f;                  /* both behind them */
   if (lo < 0.0) lo = 0.0;
   if (hi > d - 1.0) hi = d - 1.0;
   if (hi == lo) hi += 0.001;

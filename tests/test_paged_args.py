@@ -1,6 +1,7 @@
 """Argument checks of the paged-cache calls (no GPU: everything is refused on
 the host before a launch), and the host arithmetic the kernels rely on."""
 import ctypes
+import math
 import random
 
 import pytest
@@ -269,3 +270,31 @@ def test_decode_split_covers_every_unit_once():
             assert (b, hm) not in whole
             whole.add((b, hm))
         assert not pieces and len(whole) == len(items)
+
+
+# (rope_dim, theta, original length, beta_fast, beta_slow): both crossings of the
+# betas among the pairs, before them, behind them, on either side
+YARN = [(64, 1e7, 262144.0, 32.0, 1.0), (128, 1e6, 4096.0, 32.0, 1.0), (64, 10.0, 262144.0, 32.0, 1.0), (16, 1.5, 1e6, 32.0, 1.0),
+        (64, 1e4, 4.0, 32.0, 1.0), (32, 1e4, 1.0, 2.0, 1.0), (64, 10.0, 128.0, 32.0, 1.0), (64, 1e4, 300.0, 60.0, 0.01),
+        (256, 1e7, 6.0, 32.0, 1.0), (64, 1e4, 6.3, 32.0, 1.0)]
+
+
+@pytest.mark.parametrize("rope_dim,theta,length,fast,slow", YARN)
+def test_yarn_keeps_and_divides_by_the_count_of_turns(rope_dim, theta, length, fast, slow):
+    """A pair that turns at least beta_fast times over the original length keeps its
+    frequency, one of at most beta_slow turns has it divided, others lie between."""
+    _build.build(debug=True)
+    L = ctypes.CDLL(_build.LIB_DEBUG)
+    p = qsa.layer_params(head_dim=256, rope_dim=rope_dim, rope_theta=theta, yarn_factor=4.0, yarn_original_max=length,
+                         yarn_beta_fast=fast, yarn_beta_slow=slow)
+    f = (ctypes.c_double * (rope_dim // 2))()
+    assert L.qsa_debug_rope_frequencies(ctypes.byref(p), f) == 0
+    for i, got in enumerate(f):
+        plain = theta ** (-2 * i / rope_dim)
+        turns = length * plain / (2 * math.pi)
+        if turns >= fast:
+            assert got == pytest.approx(plain, rel=1e-12), i
+        elif turns <= slow:
+            assert got == pytest.approx(plain / 4, rel=1e-12), i
+        else:
+            assert plain / 4 * (1 - 1e-12) <= got <= plain * (1 + 1e-12), i
