@@ -256,8 +256,8 @@ struct Item {
   int all, n_tiles, tile0;  // tiles; those of this CTA (n_tiles from tile0 on)
   int lo, ns, n_vis;        // key number v: v < ns ? v : lo + v - ns (whole boxes)
   int first, end;           // keys needed: [first, end) and those below the sinks
-  int p0;                   // position of the first row's token
   int t0, row0;             // the sequence's first token row; first flat row of the item
+  int64_t p0;               // position of the first row's token (of any length that the call was given)
   __device__ __forceinline__ Item(const Args& x, int64_t w) {
     const PagedAttnArgs& a = x.a;
     const uint32_t per = (uint32_t)a.hq / (uint32_t)a.hk;
@@ -289,7 +289,7 @@ struct Item {
     ns = min((a.sinks + x.box - 1) / x.box * x.box, lo);
     if (ns == lo) ns = lo = 0;                      // no gap
     n_vis = ns + end - lo;
-    p0 = (int)min(pos, (int64_t)INT32_MAX);
+    p0 = pos;
     // at least one tile: rows whose keys all lie past the table come out zero
     n_tiles = all = max((n_vis + KT - 1) / KT, 1);
   }
@@ -440,13 +440,15 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
       const bool in = r0 + r < it.rows;
       const uint32_t flat = it.row0 + (in ? r0 + r : 0), row0 = it.row0, tok0 = row0 / per;
       const int shift = it.ns - it.lo;              // position -> number, behind the gap
-      const int64_t pos = (int64_t)it.p0 + (int)(flat / per - tok0);
-      const int64_t pos1 = (int64_t)it.p0 + (int)((row0 + min(it.rows, r0 + 128) - 1) / per - tok0);
-      const int64_t pos_f = (int64_t)it.p0 + (int)((row0 + min(r0, it.rows - 1)) / per - tok0);
+      const int64_t pos = it.p0 + (int)(flat / per - tok0);
+      const int64_t pos1 = it.p0 + (int)((row0 + min(it.rows, r0 + 128) - 1) / per - tok0);
+      const int64_t pos_f = it.p0 + (int)((row0 + min(r0, it.rows - 1)) / per - tok0);
       v_max = (int)min(pos + shift, (int64_t)it.n_vis - 1);
       all_max = (int)min(pos_f + shift, (int64_t)it.n_vis - 1);
-      v_min = a.window > 0 ? (int)max(pos - a.window + 1 + shift, (int64_t)0) : 0;
-      all_min = a.window > 0 ? (int)max(pos1 - a.window + 1 + shift, (int64_t)0) : 0;
+      // (numbers from n_vis on are none: a position may pass 2^31, a number may not)
+      auto from = [&](int64_t p) { return a.window > 0 ? (int)min(max(p - a.window + 1 + shift, (int64_t)0), (int64_t)it.n_vis) : 0; };
+      v_min = from(pos);
+      all_min = from(pos1);
       part = EVEN && it.n_tiles < it.all;
       orow = !in ? -1 : part ? (int64_t)(2 * cta + (it.tile0 == 0 ? 1 : 0)) * ROWS + r0 + r : it.q_row(a, per, flat);
     }

@@ -507,6 +507,30 @@ def test_window_and_sinks_of_any_size(heads, window, sinks):
     check_batch(qsa.layer_params(*heads), cache, cached, [1] * 3, q[:3], out, lse, BF)
 
 
+@pytest.mark.parametrize("heads,n", [((7, 7, 128), 300), ((16, 16, 64), 20), ((24, 2, 256), 60), ((24, 2, 256), 5)])
+@pytest.mark.parametrize("window", [8, 2 ** 31 - 100, 2 ** 31 - 1])
+@pytest.mark.parametrize("page", [64, 24])
+def test_positions_past_31_bits(heads, n, window, page):
+    """Positions that pass 2^31 lie past the table and are reported; their rows see
+    the sinks and what a window of that size leaves of the table's keys."""
+    p = qsa.layer_params(*heads, window=window, n_sinks=90)
+    cache, q, _, cu = batch(qsa.layer_params(*heads), [2 * page - 1], [1], page, BF)
+    g = gen(n)
+    q = randn(g, BF, n, *heads[::2])
+    kv = qsa.PagedKV(cache.k, cache.v, cache.table[:, :2])
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    far = 2 ** 31 - 1 - 3
+    cl = torch.tensor([far], dtype=torch.int32, device="cuda")
+    out, lse, ws = torch.empty_like(q), torch.empty(n, heads[0], device="cuda"), qsa.paged_workspace(p, 1, n)
+    qsa.qsa_paged_prefill(p, kv, 1, n, cu, cl, q, out, ws, lse=lse)
+    assert ok(ws) == 7
+    for i in some(n):
+        if i < n:
+            keys = torch.arange(2 * page)
+            keys = keys[(keys > far + i - window) | (keys < 90)].cuda()
+            U.check_row(out[i], lse[i], U.attend64(p, q[i], *cache.rows(0, keys)), BF)
+
+
 @pytest.mark.parametrize("heads", [(24, 2, 256), (28, 4, 128)])
 def test_offsets_past_the_tokens(heads):
     """Offsets beyond T count as T: nothing behind row T is read or written."""
