@@ -12,6 +12,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "qsa.h"
+#include "paged_index.h"
 #include "qsa_kernels.h"
 #include "qsa_debug.h"
 
@@ -1146,13 +1147,9 @@ qsa_status check_kv(const qsa_layer_params* p, const qsa_paged_kv* kv, int32_t B
   v.n_pages = (int32_t)kv->n_pages;
   v.page_size = kv->page_size;
   v.capacity = (int32_t)std::min<int64_t>(cap, (int64_t)1 << 30);   // key numbers stay in 32 bits
-  // division by page_size: shift s with 2^s >= page_size, multiplier
-  // floor(2^32 (2^s - page_size) / page_size) + 1
-  uint32_t sh = 0;
-  while (((int64_t)1 << sh) < kv->page_size) ++sh;
-  v.div_shift = sh;
-  v.div_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << sh) - (uint64_t)kv->page_size)) /
-                             (uint64_t)kv->page_size + 1);
+  const qsa::PageDivision d = qsa::page_division(kv->page_size);
+  v.div_mul = d.mul;
+  v.div_shift = d.shift;
   return QSA_OK;
 }
 
@@ -1418,5 +1415,14 @@ extern "C" qsa_status qsa_debug_rope_frequencies(const qsa_layer_params* p, doub
   if (!f) return QSA_ERR_INVALID_ARG;
   inv_freq(p, f);
   return QSA_OK;
+}
+extern "C" uint32_t qsa_debug_page_of(int32_t page_size, uint32_t j) {
+  const qsa::PageDivision d = qsa::page_division(page_size);
+  return qsa::page_quotient(d.mul, d.shift, j);
+}
+extern "C" int64_t qsa_debug_cut_begin(int64_t total, int64_t parts, int64_t c) { return qsa::EvenCut(total, parts).begin(c); }
+extern "C" int64_t qsa_debug_cut_owner(int64_t total, int64_t parts, int64_t u) { return qsa::EvenCut(total, parts).owner(u); }
+extern "C" int32_t qsa_debug_first_tile_slot(int32_t seq, int32_t row, int32_t T, uint32_t per, uint32_t rows) {
+  return qsa::first_tile_slot(seq, row, T, per, rows);
 }
 #endif

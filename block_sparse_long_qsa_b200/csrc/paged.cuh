@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "qsa_device.cuh"
+#include "paged_index.h"
 #include "qsa_kernels.h"
 
 namespace qsa {
@@ -51,18 +52,10 @@ template <> struct Elem<__half> {
   }
 };
 
-// x / y for 0 <= x, 0 < y: in 32 bits where both fit (a 64-bit division is a
-// routine of about a hundred instructions).
-__device__ __forceinline__ int64_t div64(int64_t x, int64_t y) {
-  if (((uint64_t)(x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
-  return x / y;
-}
-
 // ------------------------------------------------------------- page tables --
-// j / page_size for 0 <= j < 2^31 by a multiplication (round-up method of
-// Granlund and Montgomery; the constants are made on the host).
+// j / page_size for 0 <= j < 2^31
 __device__ __forceinline__ uint32_t page_of(const PagedView& c, uint32_t j) {
-  return (__umulhi(c.div_mul, j) + j) >> c.div_shift;
+  return page_quotient(c.div_mul, c.div_shift, j);
 }
 // Element offset of token j's row of KV head 0, or -1 where the table entry
 // names no page (recorded).  j must lie in [0, c.capacity).

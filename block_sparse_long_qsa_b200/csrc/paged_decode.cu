@@ -145,10 +145,8 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
   // CTAs that take part: no more than there are units, so none is without one
   const int n_cta = (int)min((int64_t)gridDim.x, total);
   const bool part = (int)blockIdx.x < n_cta;
-  // CTA c has the units from c base + min(c, more) on: base, or one more
-  const int64_t base = part ? div64(total, n_cta) : 0, more = total - base * n_cta;
-  const int64_t ua = part ? base * blockIdx.x + min((int64_t)blockIdx.x, more) : 0;
-  const int64_t ub = part ? ua + base + ((int64_t)blockIdx.x < more ? 1 : 0) : 0;
+  const EvenCut cut(total, max(n_cta, 1));
+  const int64_t ua = part ? cut.begin(blockIdx.x) : 0, ub = part ? cut.begin(blockIdx.x + 1) : 0;
   Scratch sc = scratch_of(a.scratch);
   if (tid == 0) sc.rec[blockIdx.x] = {0, 0, -1};
 
@@ -461,12 +459,8 @@ __global__ void __launch_bounds__(32 * warps_of(D), 1) paged_decode_kernel(const
       else
         *reinterpret_cast<float4*>(sc.o + ((int64_t)piece * ROWS + r) * D + c) = acc;
     }
-    if (!whole && item0 >= ua && tid == 0)
-    {
-      const int64_t u = item0 + ca.nu - 1;         // the item's last unit, and the CTA that has it
-      const int64_t last = u < more * (base + 1) ? div64(u, base + 1) : more + div64(u - more * (base + 1), base);
-      sc.rec[blockIdx.x] = {ca.b, ca.hm, (int32_t)last};
-    }
+    if (!whole && item0 >= ua && tid == 0)         // and the CTA that has the item's last unit
+      sc.rec[blockIdx.x] = {ca.b, ca.hm, (int32_t)cut.owner(item0 + ca.nu - 1)};
     __syncthreads();
     issue();                                       // the merge's slot is free
     x += n_units;

@@ -265,7 +265,7 @@ struct Item {
     const int64_t turn = div64(w, a.hk);
     g = (int)(w - turn * a.hk);
     const int slot = (int)(x.n_slots - 1 - turn), T = (int)a.T;
-    auto first_slot = [&](int seq, int row) { return (int)((uint32_t)min(max(row, 0), T) * per / M) + seq; };
+    auto first_slot = [&](int seq, int row) { return first_tile_slot(seq, row, T, per, M); };
     int l = 0, h = a.B;
     while (h - l > 1) {
       const int mid = (l + h) >> 1;
@@ -367,11 +367,10 @@ __device__ __forceinline__ Walk make_walk(const Args& x, int c, int n, void* buf
     atomicAdd(&whole[(two ? rank : tid) % n], (int)units);
   }
   __syncthreads();
-  // CTA c has the units from c base + min(c, more) on: base, or one more; CTAs
-  // beyond what is worth one have none
+  // CTAs beyond what is worth one have none
   const int64_t parts = min((int64_t)n, max(total / LEAST, (int64_t)1));
-  const int64_t base = div64(total, parts), more = total - base * parts;
-  const bool cut = __syncthreads_or(tid < n && whole[tid] > cut_cost(base));
+  const EvenCut range(total, parts);
+  const bool cut = __syncthreads_or(tid < n && whole[tid] > cut_cost(range.base));
   if (c == 0 && tid < n_items && (!cut || !units)) sc.rec[tid] = {0, -1};
   if (!cut && !two) return {c, n_items - 1, n, 0, INT32_MAX};
   if (!cut) {
@@ -380,7 +379,7 @@ __device__ __forceinline__ Walk make_walk(const Args& x, int c, int n, void* buf
     return {w, last, max(last - w, 1), 0, INT32_MAX};
   }
   if (c < parts && units) {
-    const int64_t ua = c * base + min((int64_t)c, more), ub = ua + base + (c < more ? 1 : 0);
+    const int64_t ua = range.begin(c), ub = range.begin(c + 1);
     const int64_t tile0 = at + ITEM_COST, end = tile0 + tiles;      // the item's tiles
     const int from = (int)max(ua - tile0, (int64_t)0), to = (int)max(min(ub, end) - tile0, (int64_t)0);
     if (at <= ua && ua < end) {
@@ -392,9 +391,7 @@ __device__ __forceinline__ Walk make_walk(const Args& x, int c, int n, void* buf
       out->to = to;
     }
     if (ua <= tile0 && tile0 < ub) {                                // its first tile is here
-      const int64_t u = end - 1;
-      const int64_t last = u < more * (base + 1) ? div64(u, base + 1) : more + div64(u - more * (base + 1), base);
-      sc.rec[tid] = {c, to < tiles ? (int32_t)last : -1};
+      sc.rec[tid] = {c, to < tiles ? (int32_t)range.owner(end - 1) : -1};
     }
   }
   __syncthreads();

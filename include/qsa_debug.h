@@ -50,6 +50,15 @@ qsa_status qsa_debug_inject(int32_t code);
 /* The rope_dim / 2 rotary frequencies of a layer (host array), YaRN included. */
 qsa_status qsa_debug_rope_frequencies(const qsa_layer_params* p, double* f);
 
+/* The index arithmetic that the paged-cache kernels use, on the host: j /
+ * page_size; the first unit of CTA c, and the CTA of unit u, of `total` units cut
+ * evenly over `parts` CTAs; the first tile slot of a sequence of the prefill
+ * (`per` query rows a token, `rows` of them to a tile). */
+uint32_t qsa_debug_page_of(int32_t page_size, uint32_t j);
+int64_t qsa_debug_cut_begin(int64_t total, int64_t parts, int64_t c);
+int64_t qsa_debug_cut_owner(int64_t total, int64_t parts, int64_t u);
+int32_t qsa_debug_first_tile_slot(int32_t seq, int32_t row, int32_t T, uint32_t per, uint32_t rows);
+
 #ifdef __cplusplus
 }
 #endif

@@ -298,3 +298,66 @@ def test_yarn_keeps_and_divides_by_the_count_of_turns(rope_dim, theta, length, f
             assert got == pytest.approx(plain / 4, rel=1e-12), i
         else:
             assert plain / 4 * (1 - 1e-12) <= got <= plain * (1 + 1e-12), i
+
+
+# ------------------------------ the kernels' own index arithmetic, on the host
+@pytest.fixture(scope="module")
+def debug():
+    _build.build(debug=True)
+    L = ctypes.CDLL(_build.LIB_DEBUG)
+    i32, i64, u32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32
+    L.qsa_debug_page_of.argtypes, L.qsa_debug_page_of.restype = [i32, u32], u32
+    for f in (L.qsa_debug_cut_begin, L.qsa_debug_cut_owner):
+        f.argtypes, f.restype = [i64, i64, i64], i64
+    L.qsa_debug_first_tile_slot.argtypes, L.qsa_debug_first_tile_slot.restype = [i32, i32, i32, u32, u32], i32
+    return L
+
+
+def test_page_of(debug):
+    """At the borders of pages, up to 2^31 - 1."""
+    r = random.Random(1)
+    top = (1 << 31) - 1
+    for size in list(range(1, 200)) + [544, 1000, 4095, 4096, 4097, 65535, 65536] + [r.randint(1, 65536) for _ in range(50)]:
+        js = [0, 1, size - 1, size, size + 1, top, top // size * size, top // size * size - 1]
+        js += [k * size + d for k in (r.randint(0, top // size) for _ in range(100)) for d in (-1, 0)]
+        for j in js:
+            if 0 <= j <= top:
+                assert debug.qsa_debug_page_of(size, j) == j // size, (size, j)
+
+
+def test_even_cut(debug):
+    """Every unit is one CTA's, the ranges differ by at most one, and the owner of a
+    unit is the CTA whose range holds it, for sums beyond 32 bits too."""
+    r = random.Random(2)
+    for _ in range(400):
+        parts = r.choice([1, 2, 7, 74, 148, 160])
+        total = r.choice([r.randint(0, 5), r.randint(0, 1000), r.randint(0, 1 << 45), parts, parts - 1, parts + 1])
+        begin = [debug.qsa_debug_cut_begin(total, parts, c) for c in range(parts + 1)]
+        sizes = [b - a for a, b in zip(begin, begin[1:])]
+        assert begin[0] == 0 and begin[-1] == total and max(sizes) - min(sizes) <= 1 and min(sizes) >= 0
+        for u in {0, total - 1, *(b + d for b in begin for d in (-1, 0, 1)), *(r.randint(0, max(total - 1, 0)) for _ in range(20))}:
+            if 0 <= u < total:
+                c = debug.qsa_debug_cut_owner(total, parts, u)
+                assert begin[c] <= u < begin[c + 1]
+
+
+@pytest.mark.parametrize("rows", [128, 256])
+def test_first_tile_slots(debug, rows):
+    """A sequence's tiles fit between its first slot and the next one's, the last
+    sequence's into the grid; offsets outside the tokens count as the nearer end."""
+    r = random.Random(3)
+    for _ in range(300):
+        B, per = r.randint(1, 40), r.choice([1, 2, 7, 12, 64, r.randint(1, 64)])
+        new = [r.choice([0, 0, 1, 2, r.randint(0, 300), r.randint(0, 20000)]) for _ in range(B)]
+        cu = [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+        T = cu[-1]
+        first = [debug.qsa_debug_first_tile_slot(b, cu[b], T, per, rows) for b in range(B + 1)]
+        for b in range(B):
+            assert first[b] + -(-new[b] * per // rows) <= first[b + 1]
+        assert first[B] <= -(-T * per // rows) + B
+        assert debug.qsa_debug_first_tile_slot(0, -5, T, per, rows) == 0
+        assert debug.qsa_debug_first_tile_slot(B, 2 ** 31 - 1, T, per, rows) == first[B]
+    T = (1 << 24) - 1
+    assert debug.qsa_debug_first_tile_slot(4096, T, T, 64, rows) == T * 64 // rows + 4096
