@@ -52,11 +52,12 @@ cudaError_t prepare_launch(F* kernel, uint32_t smem) {
   if (at.numRegs * THREADS < 256 * (REGS_SOFT + REGS_REST)) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
-// Quarter of a tile's exponentials after which the next tile's begin (32K tokens
-// of 24 + 2 heads of 256: 9.65 ms with 1, 9.85 with 2, 9.87 without turns; 16K of
-// 16 heads of 64: 0.95 ms with 1, 0.84 to 0.91 with 2, 0.85 with 3; 12000 of 32 + 8
-// heads of 128: 1.07 ms with 1, 1.09 with 2, 1.10 with 3).
-__host__ __device__ constexpr int turn_after(int D) { return D == 256 ? 1 : 2; }
+// Quarter of a tile's exponentials after which the next tile's begin.  Builds in turn
+// on one GPU, after quarter 1, 2 and 3: head dim 256 (24 + 2 heads) 4096 tokens 202,
+// 200 and 190 us, 8 x 500 over 2000 227, 224 and 211, 16K and 32K tokens the same within
+// 0.3 %; head dim 128 (32 + 8) 16K 2.20, 2.28 and 2.35 ms, 4096 tokens 172, 174 and
+// 178 us; head dim 64 (16) 16K 904, 858 and 882 us, 4 x 4000 273, 261 and 266.
+__host__ __device__ constexpr int turn_after(int D) { return D == 256 ? 3 : D == 128 ? 1 : 2; }
 // Lazy maximum: a tile raises it when its own exceeds it by more than RAISE, and P is
 // held times 2^P_SHIFT, so it stays below 2^(RAISE + P_SHIFT).  In fp16 (largest
 // 2^16, normal numbers from 2^-14 on) the shift keeps the bits of weights down to
