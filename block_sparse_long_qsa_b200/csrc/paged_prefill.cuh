@@ -510,6 +510,12 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
         l *= exp2_approx(m - mp);
         m = mp;
       }
+      // The P V of two tiles before is done: its P may be overwritten (where P shares
+      // the scores' columns, this tile's S came after that).  Waited for before the
+      // hand-over, because the other group's waits for this barrier's next phase go
+      // by parity: without it they could pass on the phase before and rescale, or
+      // read, an O that products are still being added to.
+      if (TM::APART && n >= 2 && !wait(&bar.pv_done[buf], ((n >> 1) - 1) & 1)) { ok = false; break; }
       const bool raise = mt > m + RAISE;
       const float m_old = m;
       if (raise) m = mt;
@@ -535,9 +541,6 @@ __device__ __forceinline__ void softmax_role(const Args& x, uint8_t* smem, uint3
           }
         }
       }
-      // the P of two tiles before has been used (where P shares the scores'
-      // columns, this tile's S came after that)
-      if (TM::APART && n >= 2 && !wait(&bar.pv_done[buf], ((n >> 1) - 1) & 1)) { ok = false; break; }
       // The exponentials of a tile begin when those of the tile before are nearly
       // done.  The two warps of a scheduler share its special-function unit: side
       // by side they would take twice as long and leave it idle afterwards.
