@@ -1211,9 +1211,9 @@ void fill_rope(const qsa_layer_params* p, qsa::RopeSpec* r) {
   *r = spec;
 }
 
-size_t paged_ws(const qsa_layer_params* p, int32_t B) {
-  return HEADER_BYTES +
-         align_up(std::max(qsa::paged_decode_scratch(p->head_dim, B), qsa::paged_prefill_scratch(p->head_dim)));
+// The scratch holds what CTAs leave for the joins: the same for any batch.
+size_t paged_ws(const qsa_layer_params* p) {
+  return HEADER_BYTES + align_up(std::max(qsa::paged_decode_scratch(p->head_dim), qsa::paged_prefill_scratch(p->head_dim)));
 }
 
 // No position is beyond 2^30: more sinks mean the same, and the kernels round them
@@ -1291,7 +1291,7 @@ qsa_status qsa_paged_workspace_size(const qsa_layer_params* p, int32_t B, int64_
   if (st != QSA_OK) return st;
   if (!bytes || B <= 0 || T < 0) return QSA_ERR_INVALID_ARG;
   if (B > MAX_PAGED_B || T >= ((int64_t)1 << 24)) return QSA_ERR_UNSUPPORTED;
-  *bytes = paged_ws(p, B);
+  *bytes = paged_ws(p);
   return QSA_OK;
 }
 
@@ -1343,7 +1343,7 @@ qsa_status qsa_paged_decode(const qsa_layer_params* p, const qsa_paged_kv* kv, i
   if (!cache_len || !q || !out || !ws) return QSA_ERR_INVALID_ARG;
   if ((int64_t)B * a.kv.capacity > ((int64_t)1 << 36)) return QSA_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(ws)) return QSA_ERR_MISALIGNED;
-  if (ws_bytes < paged_ws(p, B)) return QSA_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < paged_ws(p)) return QSA_ERR_WORKSPACE_TOO_SMALL;
   DevInfo di;
   if ((st = device_info(&di)) != QSA_OK) return st;
   a.B = B; a.hq = p->n_q_heads; a.hk = p->n_kv_heads; a.T = B;
@@ -1377,7 +1377,7 @@ qsa_status qsa_paged_prefill(const qsa_layer_params* p, const qsa_paged_kv* kv, 
   if (T == 0) return QSA_OK;
   if (!cu_new || !cache_len || !q || !out || !ws) return QSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(ws)) return QSA_ERR_MISALIGNED;
-  if (ws_bytes < paged_ws(p, B)) return QSA_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < paged_ws(p)) return QSA_ERR_WORKSPACE_TOO_SMALL;
   DevInfo di;
   if ((st = device_info(&di)) != QSA_OK) return st;
   a.B = B; a.hq = p->n_q_heads; a.hk = p->n_kv_heads; a.T = T;
@@ -1400,7 +1400,7 @@ qsa_status qsa_paged_prefill(const qsa_layer_params* p, const qsa_paged_kv* kv, 
          return qsa::launch_paged_prefill(a, tk, tv, p->head_dim, p->dtype, di.num_sms, s, false);
        }), "paged prefill launch")) != QSA_OK)
     return st;
-  if (!qsa::paged_prefill_splits(a, p->head_dim, di.num_sms)) return QSA_OK;
+  if (!qsa::paged_prefill_splits(a, p->head_dim)) return QSA_OK;
   return from_cuda(traced(QSA_KERNEL_PAGED_PREFILL_JOIN, s, [&] {
     return qsa::launch_paged_prefill(a, tk, tv, p->head_dim, p->dtype, di.num_sms, s, true);
   }), "paged prefill join launch");

@@ -561,7 +561,7 @@ cudaError_t launch_d(const PagedAttnArgs& a, int num_sms, cudaStream_t s, bool j
 
 }  // namespace
 
-size_t paged_decode_scratch(int head_dim, int) {
+size_t paged_decode_scratch(int head_dim) {
   return REC_BYTES + LSE_BYTES + (size_t)2 * MAX_CTAS * ROWS * head_dim * 4;
 }
 

@@ -15,9 +15,10 @@
 //   * warps 0-7 (softmax): two warpgroups that take the tiles in turn, a thread a
 //     query row (TMEM lane): mask, tile maximum, the running maximum from the
 //     other group (raised only when a tile exceeds it by more than 8, so the
-//     rescale of O is rare), handed back at once, then exp2 in base 2 and P
-//     packed to 16 bits into the score buffer.  So one group's exponentials run
-//     beside the other's loads and maxima.  At the end O / l and the log-sum-exp.
+//     rescale of O is rare), handed back before the exponentials (base 2), then P
+//     packed to 16 bits, for head dims 64 and 128 into TMEM columns of its own,
+//     for 256 in place of the scores.  So one group's exponentials run beside the
+//     other's loads and maxima.  At the end O / l and the log-sum-exp.
 //   * warp 13 (K): slots of 128 keys x 64 dims by TMA, a box of 16 to 64 rows of
 //     a page at a time (the numbering of the keys is rounded so that no box
 //     crosses a page).  K rows that nobody sees need no care: their scores are
@@ -39,7 +40,9 @@
 // CTAs, so a short chunk over a long prefix and batches of any mix of lengths keep
 // every SM busy.  A CTA's piece of an item that it shares goes to the scratch as
 // normalised fp32 rows with their log-sum-exp; the join kernel adds the pieces in
-// the order of the keys.  Many items are dealt out whole.
+// the order of the keys.  More items than MAX_EVEN, and pages that TMA cannot
+// fetch, are dealt out whole: there one long sequence among short ones sets the
+// time (may_cut below has the figures).
 //
 // Measured: 16384 tokens of 32 + 8 heads of 128 2.04 ms, 1080 TFLOP/s; of 16 heads
 // of 64 0.90 ms, 610 TFLOP/s.  Bound there by the exponentials: 128 x 128 of a tile
@@ -603,9 +606,13 @@ int walkers_of(const PagedAttnArgs& a, int head_dim, int num_sms) {
 // busy long after the others (64 x 5 tokens over 2000 to 30000 keys: 609 us whole,
 // 237 cut; 64 x 21: 574 and 340).  The kernel decides by the lengths; where whole items
 // are quicker after all, it costs 3 to 8 us to find out (64 tokens over 300 keys:
-// 14.4 us and 18; 16 x 100 over 1000: 66 and 74), so batches of more items than a
-// CTA has threads, which are long enough to come out even, are dealt out whole.
-bool may_cut(const PagedAttnArgs& a, int head_dim, int num_sms) {
+// 14.4 us and 18; 16 x 100 over 1000: 66 and 74).  Two limits are the walk's, which
+// counts one item a thread in a kernel that loads by TMA, and cost where lengths are
+// mixed: 64 x 5 tokens over 2000 to 30000 keys with 32 + 8 heads of 128 are 592
+// items, dealt out whole in 604 us, where 50 such sequences (482 items, 80 % of the
+// keys) are cut and take 373; 37 tokens over 20011 keys take 414 us with pages of 1, 8
+// or 24 tokens, 41 with pages of 64.
+bool may_cut(const PagedAttnArgs& a, int head_dim) {
   const int64_t items = slots_of(a, head_dim) * a.hk;
   return paged_prefill_box(a.kv.page_size) > 1 && items <= MAX_EVEN;
 }
@@ -655,7 +662,7 @@ cudaError_t launch_d(const PagedAttnArgs& a, const CUtensorMap& tk, int num_sms,
       if (use_pair(a, D)) return launch_join<E, D, 256>(x, s);
     return launch_join<E, D, 128>(x, s);
   }
-  if (may_cut(a, D, num_sms)) return launch_attn<E, D, true, true>(x, walkers, s);
+  if (may_cut(a, D)) return launch_attn<E, D, true, true>(x, walkers, s);
   return x.box > 1 ? launch_attn<E, D, true, false>(x, walkers, s) : launch_attn<E, D, false, false>(x, walkers, s);
 }
 
@@ -663,7 +670,7 @@ cudaError_t launch_d(const PagedAttnArgs& a, const CUtensorMap& tk, int num_sms,
 
 size_t paged_prefill_scratch(int head_dim) { return REC_BYTES + (size_t)2 * MAX_CTAS * 128 * (head_dim + 1) * 4; }
 
-bool paged_prefill_splits(const PagedAttnArgs& a, int head_dim, int num_sms) { return may_cut(a, head_dim, num_sms); }
+bool paged_prefill_splits(const PagedAttnArgs& a, int head_dim) { return may_cut(a, head_dim); }
 
 int paged_prefill_box(int page_size) {
   return page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : page_size % 16 == 0 ? 16 : 1;
@@ -674,7 +681,7 @@ cudaError_t launch_paged_prefill(const PagedAttnArgs& a, const CUtensorMap& tk, 
   if (a.B <= 0 || a.T <= 0) return cudaSuccess;
   if (!join && use_pair(a, head_dim)) {
     return launch_paged_prefill_pair(a, tk, tv, dtype, slots_of(a, head_dim), walkers_of(a, head_dim, num_sms),
-                                     may_cut(a, head_dim, num_sms), s);
+                                     may_cut(a, head_dim), s);
   }
   const bool bf = dtype == QSA_DTYPE_BF16;
   switch (head_dim) {

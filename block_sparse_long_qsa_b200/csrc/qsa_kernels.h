@@ -177,11 +177,11 @@ struct PagedAttnArgs {
   void* scratch;            // behind the workspace's header
   int inject;               // debug build: fault-injection code (QSA_INJECT_*), else 0
 };
-size_t paged_decode_scratch(int head_dim, int B);
+size_t paged_decode_scratch(int head_dim);
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, int head_dim, int dtype, int num_sms, cudaStream_t s,
                                 bool join);
 size_t paged_prefill_scratch(int head_dim);
-bool paged_prefill_splits(const PagedAttnArgs& a, int head_dim, int num_sms);   // whether the join is due
+bool paged_prefill_splits(const PagedAttnArgs& a, int head_dim);   // whether the join is due
 // Rows of a TMA box of the K pages, or 1: page sizes that go without TMA.
 int paged_prefill_box(int page_size);
 // tk, tv: maps of the K and V pages [n_pages][n_kv][page_size][head_dim] with

@@ -355,12 +355,17 @@ qsa_status qsa_decode_noalloc(const qsa_params* p, int32_t B, int64_t max_len, c
 qsa_status qsa_decode_noalloc_check_error(void* stream);
 
 /* ---- Layers over a paged KV cache ------------------------------------------
- * The dense and sliding-window attention layers of a model that also runs QSA
- * layers, served from a paged cache: the norms of query and key heads with the
- * rotation of positions ([PT] spec: zero-centred RMSNorm; rope_parameters
- * listing: mrope_interleaved, sections [11, 11, 10]), the append of new tokens
- * to the pages, the attention of one new token per sequence, and the attention
- * of a ragged batch of new tokens (prompts, chunks of prompts, verify steps).
+ * Dense and sliding-window attention layers served from a paged cache.  The
+ * model of the pages has none (QSA is its only global token mixer; paged dense
+ * attention is there as the baseline): these are for that baseline and for
+ * models that mix such layers with QSA ones.  Of the pages' own are the norms of
+ * query and key heads with the rotation of positions ([PT] spec: zero-centred
+ * RMSNorm; rope_parameters listing: mrope_interleaved, sections [11, 11, 10]),
+ * which feed qsa_prefill and qsa_decode too.  Beside them: the append of new
+ * tokens to the pages, the attention of one new token per sequence, and the
+ * attention of a ragged batch of new tokens (prompts, chunks of prompts, verify
+ * steps).  The QSA calls keep their contiguous caches; none of them reads these
+ * pages.
  *
  * Conventions of these calls, beside those above:
  *   - Elements are 16-bit, bf16 or fp16 by qsa_layer_params.dtype, as bit
@@ -371,7 +376,8 @@ qsa_status qsa_decode_noalloc_check_error(void* stream);
  *     replays.  They need 4-byte alignment only.
  *   - Sequence b has cache_len[b] tokens in its cache before the call's tokens;
  *     its new token i has cache position cache_len[b] + i.  cache_len[b] < 0
- *     marks a padding sequence: nothing of it is read or written.
+ *     marks a padding sequence: nothing of it is written, and neither its pages
+ *     nor its table entries are read (its rows of q, k and v may be).
  *   - Ragged batches: sequence b's new tokens are rows cu_new[b] ..
  *     cu_new[b + 1] - 1 of the token arrays (cu_new: B + 1 ascending offsets,
  *     0 <= cu_new[b] <= T).  Rows outside [cu_new[0], cu_new[B]) are left as
