@@ -1,5 +1,7 @@
 """The paged-cache calls on the GPU against 64-bit references: norms and
 rotation, append, decode, prefill, and a run of them as a server makes it."""
+import random
+
 import pytest
 import torch
 
@@ -671,6 +673,40 @@ def test_prefill_gives_the_same_bits_every_time(heads, cached, new):
         again, lse2, _ = run_prefill(p, cache, q, cl, cu, ws)
         wrong += (again != out).sum() + (lse2 != lse).sum()
     assert int(wrong) == 0 and ok(ws) == 0
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_batches(seed):
+    """Head layouts, pages, windows and lengths of any mix: some rows of each sequence
+    against 64 bits, the same bits twice, rows behind and of padding left alone."""
+    r = random.Random(seed)
+    D, per, hk = r.choice([64, 128, 256]), r.choice([1, 2, 3, 7, 12, 16, 17, 33, 64]), r.choice([1, 2, 3, 8])
+    hk, dt = min(hk, max(1, 128 // per)), r.choice([BF, FP])
+    page = r.choice([1, 8, 16, 16, 32, 48, 64, 80, r.randint(1, 200)])
+    p = qsa.layer_params(per * hk, hk, D, dtype=dt, window=r.choice([0, 0, r.randint(1, 40), r.randint(1, 2000)]),
+                         n_sinks=r.choice([0, 4, r.randint(0, 200)]), softmax_scale=r.choice([0.0, 1.0]))
+    B = r.choice([1, 1, 3, 12, 60])
+    cached = [r.choice([-1, 0, r.randint(0, 300), r.randint(0, 3000 if B < 20 else 500)]) for _ in range(B)]
+    new = [r.choice([0, 1, r.randint(0, 40), r.randint(0, 400 if B < 20 else 50)]) for _ in range(B)]
+    cached[r.randrange(B)], new[r.randrange(B)] = r.choice([0, 9001]), r.choice([1, 5, 1500])
+    layout, behind = r.choice(["token", "head", "beside"]), r.choice([0, 50])
+    cache, q, cl, cu = batch(p, cached, new, page, dt, layout, seed)
+    T = q.shape[0]
+    q = torch.cat([q, torch.zeros(behind, *q.shape[1:], dtype=dt, device="cuda")])
+    out, lse, ws = run_prefill(p, cache, q, cl, cu)
+    assert ok(ws) == 0
+    check_batch(p, cache, cached, new, q, out, lse, dt, lambda n: {0, n - 1, r.randrange(n)})
+    again, lse2, _ = run_prefill(p, cache, q, cl, cu, ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    row = 0
+    for c, n in zip(cached, new):
+        assert c >= 0 or bool((out[row:row + n] == 9).all())
+        row += n
+    assert row == T and bool((out[T:] == 9).all())
+    cache, q, cl, _ = batch(p, cached, [1] * B, page, dt, layout, seed + 1000)
+    out, lse, ws = run_decode(p, cache, q, cl)
+    assert ok(ws) == 0
+    check_batch(p, cache, cached, [1] * B, q, out, lse, dt)
 
 
 def test_prefill_bad_pages_and_rows_behind():
