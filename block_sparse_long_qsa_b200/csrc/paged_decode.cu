@@ -21,11 +21,13 @@
 // padding) and the products take a third of the time of the loads.
 //
 // Measured (24 query and 2 KV heads of 256): 64 sequences of 16K to 256K keys
-// 1.63 ms, 7.2 TB/s; 128 with a window of 4096 keys 145 us, 5.7 TB/s; one of 509
-// keys 9 us, all of it latency (two launches, a unit's loads, the join).  32 + 8
-// heads of 128, 37 sequences of up to 32K keys: 161 us, 5.4 TB/s.  40 query heads
-// of 64 on one KV head, of which an item takes 16, so the keys are read three
-// times: 176 us where one reading takes 57.
+// 1.66 ms in a replayed graph, 1.87 as single calls on fresh inputs, 7.0 and 6.3 TB/s;
+// 128 with a window of 4096 keys 148 us, 5.6 TB/s; one of 509 keys 9.5 us, all of it
+// latency (two launches, a unit's loads, the join).  32 + 8 heads of 128, 37 sequences
+// of up to 32K keys: 162 us, 5.4 TB/s.  Heads of 64: 16 + 16, 40 sequences of up to 40K
+// keys 367 to 376 us, 5.0 to 5.1 TB/s; 40 + 5, 64 sequences 158 us, 5.5 TB/s.  40 query
+// heads of 64 on one KV head, of which an item takes 16, so the keys are read three
+// times: 174 us where one reading takes 57.
 #include <cfloat>
 #include <type_traits>
 

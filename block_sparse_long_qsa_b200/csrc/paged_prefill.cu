@@ -44,11 +44,11 @@
 // fetch, are dealt out whole: there one long sequence among short ones sets the
 // time (may_cut below has the figures).
 //
-// Measured: 16384 tokens of 32 + 8 heads of 128 2.04 ms, 1080 TFLOP/s; of 16 heads
-// of 64 0.90 ms, 610 TFLOP/s.  Bound there by the exponentials: 128 x 128 of a tile
-// take the special-function units 1024 cycles, both products of 128 dims 1030, of
-// 64 dims 515.  5 tokens of 64 sequences over 2000 to 30000 keys (24 + 2 heads of
-// 256): 237 us, 5.8 TB/s of keys and values, 88 % of a copy's rate.
+// Measured: 16384 tokens of 32 + 8 heads of 128 1.96 to 2.2 ms, 1000 to 1120 TFLOP/s;
+// of 16 heads of 64 0.83 to 0.98 ms, 560 to 660 TFLOP/s (by GPU and clock).  Bound
+// there by the exponentials: 128 x 128 of a tile take the special-function units 1024
+// cycles, both products of 128 dims 1030, of 64 dims 515.  5 tokens of 64 sequences over 2000 to 30000 keys (24 + 2 heads of
+// 256): 243 to 246 us, 5.6 TB/s of keys and values, 86 % of a copy's rate.
 #include "paged_prefill.cuh"
 
 namespace qsa {
@@ -609,9 +609,9 @@ int walkers_of(const PagedAttnArgs& a, int head_dim, int num_sms) {
 // 14.4 us and 18; 16 x 100 over 1000: 66 and 74).  Two limits are the walk's, which
 // counts one item a thread in a kernel that loads by TMA, and cost where lengths are
 // mixed: 64 x 5 tokens over 2000 to 30000 keys with 32 + 8 heads of 128 are 592
-// items, dealt out whole in 604 us, where 50 such sequences (482 items, 80 % of the
-// keys) are cut and take 373; 37 tokens over 20011 keys take 414 us with pages of 1, 8
-// or 24 tokens, 41 with pages of 64.
+// items, dealt out whole in 602 us, where 50 such sequences (482 items, 80 % of the
+// keys) are cut and take 373; 37 tokens over 20011 keys take 400 to 414 us with pages
+// of 1, 8 or 24 tokens, 41 with pages of 64.
 bool may_cut(const PagedAttnArgs& a, int head_dim) {
   const int64_t items = slots_of(a, head_dim) * a.hk;
   return paged_prefill_box(a.kv.page_size) > 1 && items <= MAX_EVEN;

@@ -19,10 +19,10 @@
 // Every wait is bounded, as there; the CTAs leave together.
 // Bound by the tensor cores (a tile's products take 2060 cycles) and, over
 // milliseconds, by the power limit: 32768 tokens of 24 + 2 heads of 256 take 9.4
-// to 10.2 ms, 1290 to 1410 TFLOP/s by the clock that is left; 16384 tokens 2.3 ms
-// with the tensor pipe 75 % busy; 8 sequences of up to 8192 with a window of 1024
-// keys 0.58 ms, 960 TFLOP/s of visible pairs (the tiles at both ends of a window are
-// half masked).
+// to 9.9 ms, 1330 to 1400 TFLOP/s by the clock that is left; 16384 tokens 2.2 to 2.5 ms
+// with the tensor pipe 77 % busy; 8 sequences of up to 8192 with a window of 1024
+// keys 0.57 to 0.68 ms in a replayed graph, 0.66 as single calls on fresh inputs, 840
+// TFLOP/s of visible pairs (the tiles at both ends of a window are half masked).
 #include "paged_prefill.cuh"
 
 namespace qsa {

@@ -6,9 +6,10 @@
 //
 // with (c, s) = factor * (cos, sin)(position * f_i), one rounding at the end.
 // Bound by HBM: each element is read and written once (32768 tokens of 24 + 2
-// heads of 256: 136 us, 6.4 TB/s, 98 % of a plain copy's rate; appended with
-// their values for 13 sequences, 24472 tokens in all: 122 us, 88 %; 64 tokens:
-// 3 to 4 us, one launch's latency).
+// heads of 256: 137 us in a replayed graph, 147 as single calls on fresh inputs, 97
+// and 90 % of a plain copy's rate; appended with their values for 13 sequences,
+// 24472 tokens in all: 116 and 124 us, 92 and 86 %; 64 tokens: 3 to 5 us, one launch's
+// latency).
 #include "paged.cuh"
 
 namespace qsa {
