@@ -47,8 +47,9 @@
 // Measured: 16384 tokens of 32 + 8 heads of 128 1.96 to 2.2 ms, 1000 to 1120 TFLOP/s;
 // of 16 heads of 64 0.83 to 0.98 ms, 560 to 660 TFLOP/s (by GPU and clock).  Bound
 // there by the exponentials: 128 x 128 of a tile take the special-function units 1024
-// cycles, both products of 128 dims 1030, of 64 dims 515.  5 tokens of 64 sequences over 2000 to 30000 keys (24 + 2 heads of
-// 256): 243 to 246 us, 5.6 TB/s of keys and values, 86 % of a copy's rate.
+// cycles, both products of 128 dims 1030, of 64 dims 515.  5 tokens of 64 sequences
+// over 2000 to 30000 keys (24 + 2 heads of 256): 243 to 246 us, 5.6 TB/s of keys and
+// values, 86 % of a copy's rate.
 #include "paged_prefill.cuh"
 
 namespace qsa {
